@@ -27,7 +27,10 @@ EXPORTS = ("bdssm_abi_version", "bdssm_status_str", "bdssm_prefix_scan_workspace
            "bdssm_set_launch_override", "bdssm_prefix_scan_static",
            "bdssm_full_window_workspace", "bdssm_full_window",
            "bdssm_state_bf16_bytes", "bdssm_state_bf16", "bdssm_block_step_variant",
-           "bdssm_commit_refresh")
+           "bdssm_commit_refresh",
+           "bdssm_gated_norm", "bdssm_residual_norm",
+           "bdssm_attn_step_workspace", "bdssm_attn_step", "bdssm_kv_append")
+NORM_RMS, NORM_LAYER = 0, 1
 STATE_F32, STATE_OPS, STATE_BF16 = 0, 1, 2
 
 
@@ -62,6 +65,40 @@ class StepParams(ctypes.Structure):
 class ConvParams(ctypes.Structure):
     _fields_ = [("width", ctypes.c_int32), ("activation", ctypes.c_int32),
                 ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("rows_per_stream", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class Residual(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("o", ctypes.c_void_p), ("post_w", ctypes.c_void_p),
+                ("pre_w", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gain", ctypes.c_void_p),
+                ("shift", ctypes.c_void_p), ("mod_stride", ctypes.c_int64), ("res_scale", ctypes.c_float)]
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("nheads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("headdim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+class KvCachePtrs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_len", ctypes.c_int32)]
+
+
+class AttnChunk(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("starts", ctypes.c_void_p), ("block_len", ctypes.c_int32)]
+
+
+class AttnMask(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("block", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32)]
 
 
 _lib = None
@@ -128,6 +165,16 @@ def load():
         lib.bdssm_commit_refresh.argtypes = [P(Dims), I32, P(SeqPtrs), V, V, V, V, I32, V, V]
         lib.bdssm_set_launch_override.restype = ctypes.c_int
         lib.bdssm_set_launch_override.argtypes = [P(LaunchOverride)]
+        lib.bdssm_gated_norm.restype = ctypes.c_int
+        lib.bdssm_gated_norm.argtypes = [P(NormDims), V, V, I64, V, I32, V, V]
+        lib.bdssm_residual_norm.restype = ctypes.c_int
+        lib.bdssm_residual_norm.argtypes = [P(NormDims), P(Residual), V, V, V]
+        lib.bdssm_attn_step_workspace.restype = SZ
+        lib.bdssm_attn_step_workspace.argtypes = [P(AttnDims), I32, I32, P(AttnMask)]
+        lib.bdssm_attn_step.restype = ctypes.c_int
+        lib.bdssm_attn_step.argtypes = [P(AttnDims), P(AttnChunk), P(KvCachePtrs), P(AttnMask), V, V, SZ, V]
+        lib.bdssm_kv_append.restype = ctypes.c_int
+        lib.bdssm_kv_append.argtypes = [P(AttnDims), P(AttnChunk), P(KvCachePtrs), V, V]
         _lib = lib
     return _lib
 
@@ -366,6 +413,158 @@ class DecodeGraph:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------- norms and attention around the Mamba layers
+def _torch_dtype(dtype):
+    import torch
+    return torch.bfloat16 if dtype == BF16 else torch.float32
+
+
+def _expect(t, what, dtype, shape):
+    """A tensor argument whose sizes the library cannot see: its type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(t, what, dtype, shape):
+    """(device pointer, elements between rows) of a tensor whose rows (all dimensions but the
+    first) are contiguous; the rows themselves may be slices of longer ones."""
+    if not getattr(t, "is_cuda", False):
+        raise TypeError("bdssm takes device (CUDA/HIP) tensors only")
+    _expect(t, what, dtype, shape)
+    inner = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and step != inner:
+            raise ValueError(f"{what}: rows must be contiguous")
+        inner *= size
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
+
+
+def norm_dims(rows, width, dtype, groups=1, eps=1e-5, rows_per_stream=0, kind=NORM_RMS, x_dtype=None):
+    """A bdssm_norm_dims; x_dtype None = dtype."""
+    return NormDims(rows, width, groups, rows_per_stream, kind, dtype if x_dtype is None else x_dtype, dtype, eps)
+
+
+def gated_norm(nd, y, z, weight, out, norm_first=False, stream=None):
+    """bdssm_gated_norm: y, out [rows, width] contiguous, z rows of width channels (a slice of
+    longer rows is fine), weight [width] float32 or None."""
+    dt = _torch_dtype(nd.dtype)
+    shape = (nd.rows, nd.width)
+    zp, zs = _rows(z, "z", dt, shape)
+    for t, what, ty in ((y, "y", _torch_dtype(nd.x_dtype)), (out, "out", dt)):
+        if t.dtype != ty or t.numel() != nd.rows * nd.width:
+            raise ValueError(f"{what}: expected {ty} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if weight is not None:
+        _expect(weight, "weight", _torch_dtype(F32), shape[1:])
+    _check(load().bdssm_gated_norm(ctypes.byref(nd), _ptr(y), zp, zs, _ptr(weight), int(norm_first), _ptr(out),
+                                   _stream(stream)))
+
+
+def residual_norm(nd, x, o, pre_w, x_out, u, post_w=None, gate=None, gain=None, shift=None, res_scale=1.0,
+                  stream=None):
+    """bdssm_residual_norm: x, o, x_out, u [rows, width] contiguous (o, x_out or u may be None),
+    post_w, pre_w [width] float32 or None, gate, gain, shift [streams, width] or None (slices of
+    one projection's rows)."""
+    dt, xt, f32 = _torch_dtype(nd.dtype), _torch_dtype(nd.x_dtype), _torch_dtype(F32)
+    shape = (nd.rows, nd.width)
+    for t, what, ty in ((x, "x", xt), (o, "o", dt), (x_out, "x_out", xt), (u, "u", dt)):
+        if t is not None and (t.dtype != ty or t.numel() != nd.rows * nd.width):
+            raise ValueError(f"{what}: expected {ty} {shape}, got {t.dtype} {tuple(t.shape)}")
+    for t, what in ((post_w, "post_w"), (pre_w, "pre_w")):
+        if t is not None:
+            _expect(t, what, f32, shape[1:])
+    mods, strides = [], set()
+    for t, what in ((gate, "gate"), (gain, "gain"), (shift, "shift")):
+        if t is None:
+            mods.append(None)
+            continue
+        streams = -(-nd.rows // nd.rows_per_stream) if nd.rows_per_stream > 0 else 0
+        p, s = _rows(t, what, dt, (streams, nd.width))
+        mods.append(p)
+        strides.add(s)
+    if len(strides) > 1:
+        raise ValueError("gate, gain and shift must have one stride between streams")
+    r = Residual(_ptr(x), _ptr(o), _ptr(post_w), _ptr(pre_w), *mods, strides.pop() if strides else 0, res_scale)
+    _check(load().bdssm_residual_norm(ctypes.byref(nd), ctypes.byref(r), _ptr(x_out), _ptr(u), _stream(stream)))
+
+
+def attn_dims(batch, nheads, kv_heads, headdim, dtype, page_size):
+    return AttnDims(batch, nheads, kv_heads, headdim, dtype, page_size)
+
+
+def attn_mask(scale, block=0, window=0, sinks=0):
+    """A bdssm_attn_mask: block 0 = no order, 1 = causal, n = by blocks of n; window 0 = none."""
+    return AttnMask(scale, block, window, sinks)
+
+
+class KvCache:
+    """A paged cache as the attention calls take it: pools k, v [num_pages, kv_heads, page_size,
+    headdim], table [batch, max_pages] int32 and lens [batch] int32, all on the device, and
+    max_len, an upper bound of lens. Keeps the tensors whose addresses it holds; their contents
+    may change between calls."""
+
+    def __init__(self, ad, k, v, table, lens, max_len):
+        import torch
+        shape = (k.shape[0], ad.kv_heads, ad.page_size, ad.headdim)
+        for t, what in ((k, "k"), (v, "v")):
+            _expect(t, what, _torch_dtype(ad.dtype), shape)
+        _expect(table, "table", torch.int32, (ad.batch, table.shape[-1]))
+        _expect(lens, "lens", torch.int32, (ad.batch,))
+        self.k, self.v, self.table, self.lens = k, v, table, lens
+        self.ptrs = KvCachePtrs(_ptr(k), _ptr(v), _ptr(table), _ptr(lens), k.shape[0], table.shape[1], max_len)
+
+    @property
+    def max_len(self):
+        return self.ptrs.max_len
+
+    @max_len.setter
+    def max_len(self, n):
+        self.ptrs.max_len = n
+
+    def set_lens(self, lens):
+        """Another lengths tensor (the lens_out of an append)."""
+        import torch
+        _expect(lens, "lens", torch.int32, tuple(self.lens.shape))
+        self.ptrs.lens, self.lens = _ptr(lens), lens
+
+
+def _chunk(ad, block_len, q, k, v, starts):
+    """A bdssm_attn_chunk of q [tokens, nheads, headdim], k, v [tokens, kv_heads, headdim] (rows
+    may be slices of longer ones) and starts [batch + 1] int32 or None."""
+    dt = _torch_dtype(ad.dtype)
+    n = (q if q is not None else k).shape[0]
+    qp, qs = _rows(q, "q", dt, (n, ad.nheads, ad.headdim)) if q is not None else (None, 0)
+    kp, ks = _rows(k, "k", dt, (n, ad.kv_heads, ad.headdim)) if k is not None else (None, 0)
+    vp, vs = _rows(v, "v", dt, (n, ad.kv_heads, ad.headdim)) if v is not None else (None, 0)
+    if starts is not None:
+        import torch
+        _expect(starts, "starts", torch.int32, (ad.batch + 1,))
+    return AttnChunk(qp, kp, vp, qs, ks, vs, n, _ptr(starts), block_len)
+
+
+def attn_step_workspace(ad, block_len, max_len, mask):
+    """bdssm_attn_step_workspace (SIZE_MAX for arguments the call would reject)."""
+    return load().bdssm_attn_step_workspace(ctypes.byref(ad), block_len, max_len, ctypes.byref(mask))
+
+
+def attn_step(ad, block_len, q, k, v, cache, mask, out, workspace=None, starts=None, stream=None):
+    """bdssm_attn_step: attention of the chunk's tokens over the cache and the chunk (k = v = None:
+    over the cache alone); out [tokens, nheads, headdim] contiguous."""
+    ch = _chunk(ad, block_len, q, k, v, starts)
+    _expect(out, "out", q.dtype, q.shape)
+    _check(load().bdssm_attn_step(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(cache.ptrs), ctypes.byref(mask),
+                                  _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def kv_append(ad, block_len, k, v, cache, lens_out=None, starts=None, stream=None):
+    """bdssm_kv_append: the chunk's keys and values into the cache's pages; lens_out [batch] int32
+    receives the new lengths."""
+    if lens_out is not None:
+        _expect(lens_out, "lens_out", cache.lens.dtype, (ad.batch,))
+    ch = _chunk(ad, block_len, None, k, v, starts)
+    _check(load().bdssm_kv_append(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(cache.ptrs), _ptr(lens_out),
+                                  _stream(stream)))
 
 
 # ------------------------------------------------------------------ data movement helpers

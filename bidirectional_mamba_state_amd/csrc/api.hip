@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "bdssm.h"
+#include "host_checks.h"
 #include "internal.h"
 
 using namespace bdssm;
@@ -38,22 +39,6 @@ int device_cus()
 }  // namespace bdssm
 
 namespace {
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-Range rng(const void *p, int64_t bytes)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, p ? lo + static_cast<uintptr_t>(bytes) : lo};
-}
-
-bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elt(int dtype) { return dtype == BDSSM_BF16 ? 2 : 4; }
 
 bdssm_status check_dims(const bdssm_dims *d, Shape *s)
 {
@@ -133,8 +118,6 @@ Plan plan_prefix(const Shape &s, int64_t len, int32_t chunk, bool with_y, bool w
     p.ws_bytes = p.decay_bytes + (p.states_in_ws ? static_cast<size_t>(n_bh * NP * 4) : 0);
     return p;
 }
-
-bdssm_status launched(hipError_t e) { return e == hipSuccess ? BDSSM_OK : BDSSM_ERR_HIP; }
 
 // Launch-shape override (bdssm_set_launch_override; tests and launch-shape sweeps only):
 // block kernel choice, small-batch wavefronts per workgroup, bandwidth-kernel heads per

@@ -1,0 +1,58 @@
+// Attention over a paged cache: kernel arguments and the device-side view of a stream shared by
+// the attention kernels and the append (include/bdssm.h states the layouts and the mask).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace bdssm {
+
+struct AttnArgs {
+    const void *q, *k, *v;  // chunk rows; k, v NULL: no keys of its own
+    int64_t q_stride, k_stride, v_stride;
+    int64_t tokens;
+    const int *starts;  // NULL: uniform
+    int block_len;
+    void *kp, *vp;  // pools of pages
+    const int *table, *lens;
+    int num_pages, max_pages, max_len;
+    int batch, H, KV, page_shift;
+    float scale;
+    int block, window, sinks;
+    void *out;
+};
+
+// One stream's chunk rows and cached tokens. Every count read from device memory is brought
+// into the bounds the host knows, so that no index built from it leaves a buffer.
+struct AttnStream {
+    int64_t row0;  // first chunk row
+    int n;         // chunk tokens
+    int len;       // cached tokens
+};
+
+__device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b)
+{
+    AttnStream s;
+    const int len = a.lens[b];
+    s.len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
+    if (!a.starts) {
+        s.row0 = static_cast<int64_t>(b) * a.block_len;
+        s.n = a.block_len;
+        return s;
+    }
+    int64_t r0 = a.starts[b], r1 = a.starts[b + 1];
+    r0 = r0 < 0 ? 0 : r0 > a.tokens ? a.tokens : r0;
+    r1 = r1 < r0 ? r0 : r1 > a.tokens ? a.tokens : r1;
+    s.row0 = r0;
+    s.n = static_cast<int>(r1 - r0 < a.block_len ? r1 - r0 : a.block_len);
+    return s;
+}
+
+// whether a query at position p attends to a key at position j (both >= 0)
+__device__ __forceinline__ bool attn_sees(const AttnArgs &a, int p, int j)
+{
+    return (a.block == 0 || j / a.block <= p / a.block) && (a.window == 0 || p - j < a.window || j < a.sinks);
+}
+
+}  // namespace bdssm

@@ -433,6 +433,170 @@ bdssm_status bdssm_decode_graph_launch(const bdssm_decode_graph *graph, void *st
 void bdssm_decode_graph_destroy(bdssm_decode_graph *graph);
 
 /*
+ * The norms around a layer of the hybrid, fused with the layer's gate and with the residual
+ * update. Both calls read a row once and write each output once; sums are float32.
+ *   norm(v) = v / sqrt(mean(v^2) + eps)                        (BDSSM_NORM_RMS)
+ *   norm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)  (BDSSM_NORM_LAYER)
+ * Rows are tokens, [rows][width] row-major. Unlike the scan's tensors, every pointer of these
+ * two calls needs its element's alignment only, and width may be any number of channels (at
+ * most 16384 normalized together).
+ */
+enum { BDSSM_NORM_RMS = 0, BDSSM_NORM_LAYER = 1 };
+typedef struct {
+    int64_t rows;            /* tokens of all streams; may be 0 */
+    int32_t width;           /* channels of a row */
+    int32_t groups;          /* channel groups normalized apart, dividing width (gated norm);
+                                1 for bdssm_residual_norm */
+    int32_t rows_per_stream; /* tokens of a stream, for gate, gain and shift (else ignored) */
+    int32_t kind;            /* BDSSM_NORM_RMS, BDSSM_NORM_LAYER (residual norm only) */
+    int32_t x_dtype;         /* bdssm_dtype of y / of x and x_out; F32 or the same as dtype */
+    int32_t dtype;           /* bdssm_dtype of z and out / of o, u, gate, gain and shift */
+    float eps;               /* > 0 */
+} bdssm_norm_dims;
+
+/*
+ * The norm after a scan with the layer's gate z (a Mamba-2 layer's output norm, before its
+ * output projection), over channel groups of width / groups:
+ *   norm_first = 0   out = norm(y silu(z)) weight
+ *   norm_first = 1   out = norm(y) weight silu(z),        silu(z) = z / (1 + exp(-z))
+ *   y       [rows][width] in x_dtype (a scan's y with its heads and channels as one row)
+ *   z       [rows] rows of width channels in dtype, z_stride elements apart (>= width): a
+ *           slice of the input projection's rows
+ *   weight  [width] float32, or NULL for ones
+ *   out     [rows][width] in dtype; may be y itself when the types are the same, must not
+ *           overlap anything else
+ * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (dtypes, kind, eps, more than
+ * 16384 channels in a group), BDSSM_ERR_ALIGN, BDSSM_ERR_ALIAS, BDSSM_ERR_HIP.
+ */
+bdssm_status bdssm_gated_norm(const bdssm_norm_dims *dims, const void *y, const void *z, int64_t z_stride,
+                              const float *weight, int32_t norm_first, void *out, void *stream);
+
+/*
+ * The residual update between two blocks: the norm after the block that ends, its gate and
+ * residual scale, the addition, and the norm before the block that begins, with the timestep's
+ * gain and shift (AdaLN: gamma_t norm(x) + beta_t; "Breaking the Bottleneck with DiffuApriel",
+ * Sec. 3.2, eqs. (7)-(9)):
+ *   t = norm(o) post_w (o itself when post_w is NULL)
+ *   r = x + res_scale * gate[s] t
+ *   u = norm(r) pre_w gain[s] + shift[s]            s = row / rows_per_stream
+ *   x          [rows][width] in x_dtype: the residual stream
+ *   o          [rows][width] in dtype: the block's output, or NULL for r = x
+ *   post_w, pre_w      [width] float32, or NULL (no post norm; ones)
+ *   gate, gain, shift  per stream [width] in dtype, mod_stride elements from stream to stream
+ *                      (slices of one projection of the timestep), each or NULL (1, 1, 0)
+ *   x_out      [rows][width] in x_dtype: r; may be x itself; NULL = not wanted
+ *   u          [rows][width] in dtype: the next block's input; NULL = not wanted (one of the
+ *              two is required). u is taken from r before r is rounded to x_dtype.
+ * Outputs must not overlap anything but x_out == x. Errors as bdssm_gated_norm.
+ */
+typedef struct {
+    const void *x, *o;
+    const float *post_w, *pre_w;
+    const void *gate, *gain, *shift;
+    int64_t mod_stride;
+    float res_scale;
+} bdssm_residual;
+bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const bdssm_residual *r, void *x_out, void *u,
+                                 void *stream);
+
+/*
+ * Attention layers of the hybrid. A block-diffusion hybrid puts an attention layer between
+ * groups of Mamba layers; its cache is the keys and values K_{1:k-1}, V_{1:k-1} of the
+ * committed blocks (eq. (6) of "Training Hybrid Block Diffusion Language Models with Partial
+ * Bidirectionality"), and its step and commit are to that cache what bdssm_block_step and
+ * bdssm_commit are to the state: the step reads the cache and never writes it, the commit
+ * (bdssm_kv_append) appends the finished block's keys and values.
+ *
+ * Paged cache: keys and values live in two pools of pages
+ *     [num_pages][kv_heads][page_size][headdim],
+ * and stream b's cached token j is slot j % page_size of page table[b][j / page_size]. An entry
+ * outside [0, num_pages) is a page the stream does not hold (one given back): its tokens are
+ * not attended to, and appends to it are dropped. lens[b] tokens of stream b are cached; lens
+ * below 0 or above max_len are taken as 0 and max_len. Slots past a stream's length are never
+ * used, whatever they hold.
+ *
+ * Chunk: the new tokens of every stream, rows of [heads][headdim] a stride apart (slices of one
+ * projection). With starts NULL, stream b has the block_len rows from b * block_len; else the
+ * rows starts[b] .. starts[b+1]-1 (ascending, at most block_len of them, which may be 0; a
+ * longer stream's rows past block_len, and rows past `tokens`, are not computed).
+ *
+ * Chunk token i of stream b is at position p = lens[b] + i, cached token j at position j. A
+ * query at p attends to key j (cached or of the chunk itself) when
+ *     block = 0   always               block > 0   j / block <= p / block   (1: causal;
+ *                                      32: whole blocks of 32, causal between them)
+ * and window = 0 or p - j < window or j < sinks (a sliding window that looks `window` tokens
+ * back, its own among them, beside the first `sinks` tokens). The softmax is over scale * q.k,
+ * its maximum, sum and the weighted sum of values in float32; with bf16 values each weight is
+ * rounded to bf16 for the matrix product. A query that attends to nothing gets zeros. Keys and
+ * values that no query of a stream attends to may hold anything.
+ */
+typedef struct {
+    int32_t batch;     /* streams */
+    int32_t nheads;    /* query heads, a multiple of kv_heads: head h reads KV head
+                          h / (nheads / kv_heads) */
+    int32_t kv_heads;
+    int32_t headdim;   /* 64 or 128 */
+    int32_t dtype;     /* bdssm_dtype of q, k, v, the pages and out */
+    int32_t page_size; /* tokens per page: 16, 32, 64, 128 or 256 */
+} bdssm_attn_dims;
+
+typedef struct {
+    void *k, *v;          /* pools of pages; written by bdssm_kv_append only */
+    const int32_t *table; /* [batch][max_pages] device page numbers */
+    const int32_t *lens;  /* [batch] device cached tokens */
+    int32_t num_pages;    /* pages in each pool */
+    int32_t max_pages;    /* entries of a table row */
+    int32_t max_len;      /* upper bound of lens (known on the host; sizes the launch);
+                             at most max_pages * page_size */
+} bdssm_kv_cache;
+
+typedef struct {
+    const void *q, *k, *v;              /* first rows; q unused by bdssm_kv_append */
+    int64_t q_stride, k_stride, v_stride; /* elements between rows, multiples of 16 bytes */
+    int64_t tokens;                     /* rows of q, k, v and out (batch * block_len when
+                                           starts is NULL) */
+    const int32_t *starts;              /* [batch + 1] device row offsets, or NULL */
+    int32_t block_len;                  /* tokens of a stream, or the most of any */
+} bdssm_attn_chunk;
+
+typedef struct {
+    float scale;    /* of q.k, e.g. 1 / sqrt(headdim) */
+    int32_t block;  /* 0: no order; else tokens of a block (>= 1) */
+    int32_t window; /* 0: none; else >= 1 */
+    int32_t sinks;  /* >= 0; first tokens outside the window that stay visible */
+} bdssm_attn_mask;
+
+/*
+ * Attention of the chunk's tokens over the cache and the chunk itself (cache and chunk are
+ * only read).
+ *   chunk->k, chunk->v  both NULL: the chunk has no keys of its own, the queries attend to the
+ *             cache alone (then a mask can leave a query nothing)
+ *   out       [tokens][nheads][headdim] in dtype; must not overlap anything
+ *   workspace at least bdssm_attn_step_workspace(...) bytes for block_len, max_len and mask:
+ *             partial results of a long cache that is split over workgroups
+ * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (headdim, page_size, dtype),
+ * BDSSM_ERR_ALIGN (base pointers and row strides to 16 bytes; table, lens and starts to 4),
+ * BDSSM_ERR_ALIAS, BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The workspace query returns SIZE_MAX
+ * for arguments the call would reject.
+ */
+size_t bdssm_attn_step_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len,
+                                 const bdssm_attn_mask *mask);
+bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_kv_cache *cache,
+                             const bdssm_attn_mask *mask, void *out, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * The commit of an attention layer: the chunk's keys and values become cached tokens
+ * lens[b] .. lens[b] + n_b - 1 of their stream (tokens past the table's last page are dropped).
+ *   lens_out  [batch] int32: the new lengths, min(lens[b] + n_b, max_pages * page_size), or
+ *             NULL; must not overlap lens, since every workgroup reads it (a caller swaps the
+ *             two). max_len bounds the lengths before the append.
+ * Errors as bdssm_attn_step.
+ */
+bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_kv_cache *cache,
+                             int32_t *lens_out, void *stream);
+
+/*
  * Launch-shape override, for tests and launch-shape sweeps only (not for the hot path).
  * Several kernels implement the block step, each one in full and each checked against the
  * same bounds; the library picks one per call from the shapes. This call pins that choice
