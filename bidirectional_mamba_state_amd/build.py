@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libbdssm.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "scan_valu.hip", "block_step_mfma.hip", "block_step_lat.hip", "block_step_bw.hip",
-           "prefix_mfma.hip", "graph.hip", "conv.hip", "norm.hip", "attn.hip"]
+           "prefix_mfma.hip", "graph.hip", "conv.hip", "norm.hip", "attn.hip",
+           "attn_mfma.hip"]
 ARCH = "gfx950"
 
 COMPILE = [

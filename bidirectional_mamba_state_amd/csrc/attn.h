@@ -49,10 +49,14 @@ __device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b)
     return s;
 }
 
-// whether a query at position p attends to a key at position j (both >= 0)
-__device__ __forceinline__ bool attn_sees(const AttnArgs &a, int p, int j)
-{
-    return (a.block == 0 || j / a.block <= p / a.block) && (a.window == 0 || p - j < a.window || j < a.sinks);
-}
+// Launch plan of a step: row tiles per (stream, KV head), ranges that the keys are split into,
+// and the workspace of the partial results (maxima and sums first, then rows; 0 unless split).
+struct AttnPlan {
+    int nrt, nsplit;
+    size_t ml_bytes, ws_bytes;
+};
+
+AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);
+hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 
 }  // namespace bdssm

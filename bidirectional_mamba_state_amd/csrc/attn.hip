@@ -10,84 +10,6 @@
 namespace bdssm {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v)
-{
-    return static_cast<float>(v);
-}
-
-// Simple form: one wavefront per (token, query head). Per 64 keys, lane j takes key j's whole
-// dot product, the running maximum and sum are updated once, and the weighted values are summed
-// with the channels spread over the lanes.
-template <typename T, int D>
-__global__ __launch_bounds__(64) void k_attn_rows(AttnArgs a)
-{
-    constexpr int C = D / 64;  // channels per lane
-    const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x;
-    const AttnStream s = attn_stream(a, b);
-    if (i >= s.n)
-        return;
-    __shared__ float qs[D];
-    const int kvh = h / (a.H / a.KV), p = s.len + i;
-    const T *q = static_cast<const T *>(a.q) + (s.row0 + i) * a.q_stride + static_cast<int64_t>(h) * D;
-    for (int d = lane; d < D; d += 64)
-        qs[d] = to_f(q[d]) * a.scale;
-    __syncthreads();
-    float m = -__builtin_inff(), l = 0.f, acc[C] = {};
-    const int page = 1 << a.page_shift, total = s.len + (a.k ? s.n : 0);
-    for (int j0 = 0; j0 < total; j0 += 64) {
-        const int j = j0 + lane;
-        const T *kr = nullptr, *vr = nullptr;
-        if (j < s.len) {
-            const int pg = a.table[static_cast<int64_t>(b) * a.max_pages + (j >> a.page_shift)];
-            if (pg >= 0 && pg < a.num_pages) {
-                const int64_t off = ((static_cast<int64_t>(pg) * a.KV + kvh) * page + (j & (page - 1))) * D;
-                kr = static_cast<const T *>(a.kp) + off;
-                vr = static_cast<const T *>(a.vp) + off;
-            }
-        } else if (j < total) {
-            kr = static_cast<const T *>(a.k) + (s.row0 + j - s.len) * a.k_stride + static_cast<int64_t>(kvh) * D;
-            vr = static_cast<const T *>(a.v) + (s.row0 + j - s.len) * a.v_stride + static_cast<int64_t>(kvh) * D;
-        }
-        const bool see = kr && attn_sees(a, p, j);
-        float sc = -__builtin_inff();
-        if (see) {
-            sc = 0.f;
-            for (int d = 0; d < D; ++d)
-                sc = fmaf(qs[d], to_f(kr[d]), sc);
-        }
-        float mx = sc;
-        for (int o = 32; o; o >>= 1)
-            mx = fmaxf(mx, __shfl_xor(mx, o));
-        if (mx == -__builtin_inff())
-            continue;  // nothing visible in these 64
-        const float mn = fmaxf(m, mx), f = __expf(m - mn), w = __expf(sc - mn);
-        m = mn;
-        float ws = w;
-        for (int o = 32; o; o >>= 1)
-            ws += __shfl_xor(ws, o);
-        l = l * f + ws;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            acc[c] *= f;
-        unsigned long long mask = __ballot(see);
-        while (mask) {
-            const int t = __builtin_ctzll(mask);
-            mask &= mask - 1;
-            const float wt = __shfl(w, t);
-            const T *vt = reinterpret_cast<const T *>(__shfl(reinterpret_cast<long long>(vr), t));
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                acc[c] = fmaf(wt, to_f(vt[lane + 64 * c]), acc[c]);
-        }
-    }
-    T *o = static_cast<T *>(a.out) + ((s.row0 + i) * a.H + h) * D;
-    const float r = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-        o[lane + 64 * c] = static_cast<T>(acc[c] * r);
-}
-
 // Append: one thread copies a 16-byte piece of a token's keys and the same piece of its values
 // (pieces run over [KV][D] of a token, so a wavefront reads whole lines of the chunk's rows and
 // writes whole lines of a head's page). Streams along y; nothing but the copy's bytes bounds it.
@@ -117,6 +39,12 @@ __global__ __launch_bounds__(256) void k_append(AttnArgs a, int *lens_out, int h
     static_cast<uint4 *>(a.vp)[to] = vx;
 }
 
+// Positions and row numbers are 32-bit integers in the kernels, offsets inside eight rows too.
+constexpr int64_t kMaxPosition = INT_MAX - 1024, kMaxStride = 1 << 24;
+
+// rows (token, head of a group) of a stream, and with them the grid's threads
+bool rows_fit(const AttnArgs &a) { return static_cast<int64_t>(a.block_len) * (a.H / a.KV) <= 1 << 30; }
+
 bdssm_status check_attn_dims(const bdssm_attn_dims *d)
 {
     if (!d)
@@ -129,7 +57,7 @@ bdssm_status check_attn_dims(const bdssm_attn_dims *d)
         return BDSSM_ERR_UNSUPPORTED;
     if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128 && d->page_size != 256)
         return BDSSM_ERR_UNSUPPORTED;
-    if (d->nheads > 65535 || d->batch > 65535)
+    if (d->nheads > 512 || d->batch > 65535)
         return BDSSM_ERR_UNSUPPORTED;
     return BDSSM_OK;
 }
@@ -140,7 +68,7 @@ bdssm_status check_attn_mask(const bdssm_attn_mask *m)
         return BDSSM_ERR_NULL;
     if (m->block < 0 || m->window < 0 || m->sinks < 0)
         return BDSSM_ERR_SHAPE;
-    if (!(m->scale == m->scale) || m->scale - m->scale != 0.f)  // NaN or infinite
+    if (!(m->scale > 0.f) || m->scale - m->scale != 0.f)  // not positive, NaN or infinite
         return BDSSM_ERR_UNSUPPORTED;
     return BDSSM_OK;
 }
@@ -168,8 +96,8 @@ bdssm_status prepare_attn(const bdssm_attn_dims *d, const bdssm_attn_chunk *ch, 
     const int64_t held = static_cast<int64_t>(ca->max_pages) * d->page_size;
     if (ca->max_len > held)
         return BDSSM_ERR_SHAPE;
-    // positions and row numbers are 32-bit integers in the kernels
-    if (static_cast<int64_t>(ca->max_len) + ch->block_len > INT_MAX - 256 || ch->tokens > INT_MAX)
+    if (static_cast<int64_t>(ca->max_len) + ch->block_len > kMaxPosition || ch->tokens > INT_MAX ||
+        ch->q_stride > kMaxStride || ch->k_stride > kMaxStride || ch->v_stride > kMaxStride)
         return BDSSM_ERR_UNSUPPORTED;
     // an empty tensor may have no address
     if (ch->tokens > 0 && ((need_q && !ch->q) || (need_kv && !ch->k) || !ch->k != !ch->v))
@@ -207,17 +135,6 @@ bdssm_status prepare_attn(const bdssm_attn_dims *d, const bdssm_attn_chunk *ch, 
     return BDSSM_OK;
 }
 
-template <typename T>
-hipError_t launch_rows(const AttnArgs &a, int D, hipStream_t st)
-{
-    const dim3 g(a.block_len, a.H, a.batch);
-    if (D == 64)
-        k_attn_rows<T, 64><<<g, 64, 0, st>>>(a);
-    else
-        k_attn_rows<T, 128><<<g, 64, 0, st>>>(a);
-    return hipGetLastError();
-}
-
 }  // namespace
 }  // namespace bdssm
 
@@ -226,9 +143,18 @@ using namespace bdssm;
 extern "C" size_t bdssm_attn_step_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len,
                                             const bdssm_attn_mask *mask)
 {
-    if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK || block_len < 0 || max_len < 0)
+    if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK || block_len < 0 || max_len < 0 ||
+        static_cast<int64_t>(max_len) + block_len > kMaxPosition)
         return SIZE_MAX;
-    return 0;
+    if (dims->batch == 0 || block_len == 0)
+        return 0;
+    AttnArgs a{};
+    a.batch = dims->batch, a.H = dims->nheads, a.KV = dims->kv_heads;
+    a.block_len = block_len, a.max_len = max_len;
+    a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
+    if (!rows_fit(a))
+        return SIZE_MAX;
+    return attn_plan(a, dims->headdim, dims->dtype == BDSSM_BF16).ws_bytes;
 }
 
 extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,
@@ -254,9 +180,19 @@ extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm
         return BDSSM_OK;
     a.scale = mask->scale, a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
     a.out = out;
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    return launched(dims->dtype == BDSSM_BF16 ? launch_rows<__bf16>(a, dims->headdim, st)
-                                              : launch_rows<float>(a, dims->headdim, st));
+    if (!rows_fit(a))
+        return BDSSM_ERR_UNSUPPORTED;
+    const bool bf16 = dims->dtype == BDSSM_BF16;
+    const AttnPlan p = attn_plan(a, dims->headdim, bf16);
+    if (p.ws_bytes > 0) {
+        if (!workspace || workspace_bytes < p.ws_bytes)
+            return BDSSM_ERR_WORKSPACE;
+        const Range rw = rng(workspace, static_cast<int64_t>(p.ws_bytes));
+        for (Range q : {r.q, r.k, r.v, r.kp, r.vp, r.table, r.lens, r.starts, ro})
+            if (overlap(rw, q))
+                return BDSSM_ERR_ALIAS;
+    }
+    return launched(launch_attn(a, dims->headdim, bf16, p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 extern "C" bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,

@@ -532,8 +532,8 @@ bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const bdssm_residu
  */
 typedef struct {
     int32_t batch;     /* streams */
-    int32_t nheads;    /* query heads, a multiple of kv_heads: head h reads KV head
-                          h / (nheads / kv_heads) */
+    int32_t nheads;    /* query heads, at most 512, a multiple of kv_heads: head h reads KV
+                          head h / (nheads / kv_heads) */
     int32_t kv_heads;
     int32_t headdim;   /* 64 or 128 */
     int32_t dtype;     /* bdssm_dtype of q, k, v, the pages and out */
@@ -552,7 +552,8 @@ typedef struct {
 
 typedef struct {
     const void *q, *k, *v;              /* first rows; q unused by bdssm_kv_append */
-    int64_t q_stride, k_stride, v_stride; /* elements between rows, multiples of 16 bytes */
+    int64_t q_stride, k_stride, v_stride; /* elements between rows, multiples of 16 bytes, at
+                                             most 2^24 */
     int64_t tokens;                     /* rows of q, k, v and out (batch * block_len when
                                            starts is NULL) */
     const int32_t *starts;              /* [batch + 1] device row offsets, or NULL */
@@ -560,7 +561,7 @@ typedef struct {
 } bdssm_attn_chunk;
 
 typedef struct {
-    float scale;    /* of q.k, e.g. 1 / sqrt(headdim) */
+    float scale;    /* of q.k, > 0: e.g. 1 / sqrt(headdim) */
     int32_t block;  /* 0: no order; else tokens of a block (>= 1) */
     int32_t window; /* 0: none; else >= 1 */
     int32_t sinks;  /* >= 0; first tokens outside the window that stay visible */
