@@ -49,11 +49,16 @@ __device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b)
     return s;
 }
 
-// Launch plan of a step: row tiles per (stream, KV head), ranges that the keys are split into,
-// and the workspace of the partial results (maxima and sums first, then rows; 0 unless split).
+// Launch plan of a step. A unit is one (stream, KV head, range of its keys); its row tiles read
+// the same keys, so they go to one XCD (its L2 then fetches them once), side by side in time.
+// Few units with many row tiles are cut into `sub` parts of every sub-th tile, so that all eight
+// XCDs have work. Workgroup id: XCD id % 8, and inside an XCD row tiles run fastest (rt_fast) or
+// slowest.
 struct AttnPlan {
-    int nrt, nsplit;
-    size_t ml_bytes, ws_bytes;
+    int nrt, nsplit;                  // row tiles per (stream, KV head); ranges of its keys
+    int sub, nrt_sub, units, per_xcd; // parts per unit, row tiles per part, parts, parts per XCD
+    int rt_fast;
+    size_t ml_bytes, ws_bytes;        // workspace: maxima and sums first, then rows (0 unless split)
 };
 
 AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);

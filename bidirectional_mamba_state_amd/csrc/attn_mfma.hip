@@ -26,9 +26,11 @@
 // free of bank conflicts. NST stages: NST - 1 tiles are in flight while one is computed.
 //
 // Masks. Per tile a 64-bit mask says which keys exist, are held and are attended to by any row
-// of the workgroup. Tiles that every row of a wavefront sees whole skip all checks; in the
-// others scores are selected per element and the values of absent keys are cleared in
-// registers (they may hold anything, NaN included).
+// of the workgroup; the values of the others (which may hold anything, NaN included) are cleared
+// in LDS before use. Scores are selected per element in tiles that some row of a wavefront does
+// not see whole; the other tiles skip that.
+#include <algorithm>
+
 #include "attn.h"
 #include "internal.h"
 #include "mfma_tiles.h"
@@ -87,6 +89,9 @@ __device__ __forceinline__ float half_sum(float v)
     return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// the n lowest bits, for any n
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
 template <int N>
 struct Int {
     static constexpr int value = N;
@@ -100,7 +105,7 @@ struct AttnCfg {
 
 template <typename T, int D, int QT, int WM, int WK, int TK, int NST, int WPE>
 __global__ __launch_bounds__((AttnCfg<T, D, QT, WM, WK, TK, NST>::THREADS))
-__attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, int nsplit, float *part, float2 *part_ml)
+__attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan pl, float *part, float2 *part_ml)
 {
     using C = AttnCfg<T, D, QT, WM, WK, TK, NST>;
     using L = Tile<T, D>;
@@ -122,8 +127,18 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
 
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / WK, wk = w % WK, hf = lane >> 5, l32 = lane & 31;
-    const int b = blockIdx.z, kvh = blockIdx.y % a.KV, split = blockIdx.y / a.KV, G = a.H / a.KV;
-    const int rt = a.block ? nrt - 1 - blockIdx.x : blockIdx.x;  // ordered: the longest ranges first
+
+    // ---- this workgroup's part, row tile and unit (see AttnPlan)
+    const int nsplit = pl.nsplit, wid = blockIdx.x >> 3;
+    const int part_no = (pl.rt_fast ? wid / pl.nrt_sub : wid % pl.per_xcd) * 8 + (blockIdx.x & 7);
+    if (part_no >= pl.units)
+        return;
+    const int per_sub = pl.units / pl.sub, u = part_no % per_sub;
+    const int rt_up = (pl.rt_fast ? wid % pl.nrt_sub : wid / pl.per_xcd) * pl.sub + part_no / per_sub;
+    if (rt_up >= pl.nrt)
+        return;
+    const int rt = a.block ? pl.nrt - 1 - rt_up : rt_up;  // ordered: the longest ranges first
+    const int kvh = u % a.KV, split = u / a.KV % nsplit, b = u / a.KV / nsplit, G = a.H / a.KV;
     const AttnStream s = attn_stream(a, b);
     const int rows = s.n * G, r_first = rt * C::RT;
     if (r_first >= rows)
@@ -180,44 +195,50 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
         }
     };
     const int crow = lane / PPR, cslot = lane % PPR;  // row of a copy, LDS piece of that row
-    const char *kp = static_cast<const char *>(a.kp), *vp = static_cast<const char *>(a.vp);
+    const int page_bytes = page * ROWB;
+    const uint32_t pool_step = static_cast<uint32_t>(a.KV * page_bytes);  // from page to page
+    const char *kp = static_cast<const char *>(a.kp) + static_cast<int64_t>(kvh) * page_bytes;
+    const char *vp = static_cast<const char *>(a.vp) + static_cast<int64_t>(kvh) * page_bytes;
     const char *ck = static_cast<const char *>(a.k) + (s.row0 * a.k_stride + static_cast<int64_t>(kvh) * D) * EL;
     const char *cv = static_cast<const char *>(a.v) + (s.row0 * a.v_stride + static_cast<int64_t>(kvh) * D) * EL;
-    const int page_bytes = page * ROWB;
     uint64_t valid[NST][PIDS];  // per stage: the tile's keys that exist and that some row attends to
     auto copy = [&](auto S, int t, const int (&ids)[PIDS]) {
         const Where x = where(t);
 #pragma unroll
         for (int i = 0; i < PIDS; ++i) {
             const int kk = 64 * i + lane, j = x.cached ? x.start + kk : s.len + x.start + kk;
-            const bool there = x.cached ? j < s.len && ids[i] >= 0 && ids[i] < a.num_pages : x.start + kk < n;
-            valid[S.value][i] = __ballot(kk < TK && there && j < hi_max && (j >= lo_min || j < a.sinks));
+            const bool held = static_cast<uint32_t>(ids[i]) < static_cast<uint32_t>(a.num_pages);
+            const bool there = x.cached ? (j < s.len) & held : x.start + kk < n;
+            valid[S.value][i] = __ballot((kk < TK) & there & (j < hi_max) & ((j >= lo_min) | (j < a.sinks)));
         }
+        if (x.cached) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int row0 = (w + NW * c) * RPC, row = row0 + crow;
-            const int kpc = cslot ^ L::swz_k(row), vpc = cslot ^ L::swz_v(row);
-            char *kd = KBUF(S) + row0 * ROWB, *vd = VBUF(S) + row0 * ROWB;
-            if (x.cached) {
-                const int pg = __builtin_amdgcn_readlane(ids[RPC * NW * c / 64], row0 % 64);  // RPC NW divides 64
-                const bool ok = pg >= 0 && pg < a.num_pages;
-                const int64_t base = (static_cast<int64_t>(ok ? pg : 0) * a.KV + kvh) * page_bytes;
-                const int off = ((x.start + row0) & (page - 1)) * ROWB + crow * ROWB;
+            for (int c = 0; c < NC; ++c) {
+                const int row0 = (w + NW * c) * RPC, row = row0 + crow;
+                const uint32_t pg = __builtin_amdgcn_readlane(ids[RPC * NW * c / 64], row0 % 64);  // RPC NW divides 64
                 // a page that is not held: an empty range, nothing is read
-                copy_to_lds(buffer_range(kp + base, ok ? page_bytes : 0), kd, off + kpc * 16);
-                copy_to_lds(buffer_range(vp + base, ok ? page_bytes : 0), vd, off + vpc * 16);
-            } else {
+                const bool ok = pg < static_cast<uint32_t>(a.num_pages);
+                const uint64_t base = ok ? static_cast<uint64_t>(pg) * pool_step : 0;
+                const int off = ((x.start + row0) & (page - 1)) * ROWB + crow * ROWB;
+                copy_to_lds(buffer_range(kp + base, ok ? page_bytes : 0), KBUF(S) + row0 * ROWB,
+                            off + (cslot ^ L::swz_k(row)) * 16);
+                copy_to_lds(buffer_range(vp + base, ok ? page_bytes : 0), VBUF(S) + row0 * ROWB,
+                            off + (cslot ^ L::swz_v(row)) * 16);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int row0 = (w + NW * c) * RPC, row = row0 + crow;
                 // rows past the chunk's end: its last row again
                 const int i0 = x.start + row0 < n ? x.start + row0 : n - 1;
                 const int dr = i0 + crow < n ? crow : n - 1 - i0;
-                copy_to_lds(buffer_range(ck + i0 * a.k_stride * EL, 0x7fffffff), kd,
-                            dr * static_cast<int>(a.k_stride) * EL + kpc * 16);
-                copy_to_lds(buffer_range(cv + i0 * a.v_stride * EL, 0x7fffffff), vd,
-                            dr * static_cast<int>(a.v_stride) * EL + vpc * 16);
+                copy_to_lds(buffer_range(ck + i0 * a.k_stride * EL, 0x7fffffff), KBUF(S) + row0 * ROWB,
+                            dr * static_cast<int>(a.k_stride) * EL + (cslot ^ L::swz_k(row)) * 16);
+                copy_to_lds(buffer_range(cv + i0 * a.v_stride * EL, 0x7fffffff), VBUF(S) + row0 * ROWB,
+                            dr * static_cast<int>(a.v_stride) * EL + (cslot ^ L::swz_v(row)) * 16);
             }
         }
     };
-
     // the copies of tile t, and ahead of them (memory operations complete in order) the page
     // numbers of the next tile
     auto start = [&](auto S, int t) {
@@ -251,43 +272,59 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
         m[i] = -__builtin_inff(), l[i] = 0.f;
     const float sc = a.scale * kLog2e;
 
-    // the 32 bits of a tile's key mask that belong to 32-key block blk
-    auto bits_of = [](const uint64_t (&ok)[PIDS], int blk) {
-        return static_cast<uint32_t>((blk < 2 ? ok[0] : ok[PIDS - 1]) >> (32 * (blk & 1)));
-    };
+    // ---- operand reads. Every lane offset is one opaque value, a single step from its array:
+    // the compiler then sees which array a read is from, and does not make it wait for copies
+    // into the others.
+    int koff[L::STEPS], voff[sizeof(T) == 2 ? D / 32 : 1];
+#pragma unroll
+    for (int st = 0; st < L::STEPS; ++st) {
+        koff[st] = (32 * wk * KB + l32) * ROWB + (((2 * st + hf) ^ L::swz_k(l32)) * 16);
+        asm volatile("" : "+v"(koff[st]));
+    }
+    if constexpr (EL == 2) {
+        const int j16 = lane & 15, cg = (lane >> 4) & 1;  // lane of a 16-lane group, column half
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+            const int pc = (4 * d + 2 * cg + ((j16 & 3) >> 1)) ^ L::swz_v(j16 >> 2);
+            voff[d] = (32 * wk * KB + 4 * hf + (j16 >> 2)) * ROWB + pc * 16 + (j16 & 1) * 8;
+            asm volatile("" : "+v"(voff[d]));
+        }
+    } else {
+        voff[0] = (32 * wk * KB + 4 * hf) * ROWB + l32 * 4;
+        asm volatile("" : "+v"(voff[0]));
+    }
 
     // ---- one tile, this wavefront's KB blocks of 32 keys
-    auto compute = [&](auto S, auto MASKED, int jpos, const uint64_t (&ok)[PIDS]) {
-        const char *kt = KBUF(S), *vt = VBUF(S);
+    auto compute = [&](auto S, bool whole, int jpos) {
         f32x16 sv[KB][QT];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
             for (int i = 0; i < QT; ++i)
                 sv[kb][i] = f32x16{};
-            const int row = 32 * (wk * KB + kb) + l32;
-            const char *kr = kt + row * ROWB;
 #pragma unroll
             for (int st = 0; st < L::STEPS; ++st) {
-                const Frag kf = *reinterpret_cast<const Frag *>(kr + (((2 * st + hf) ^ L::swz_k(l32)) * 16));
+                const Frag kf = *reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * kb * ROWB]);
 #pragma unroll
                 for (int i = 0; i < QT; ++i)
                     sv[kb][i] = L::qk(kf, q[i][st], sv[kb][i]);
             }
         }
-        if (MASKED.value) {
+        if (!whole) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const int blk = wk * KB + kb;
-                const uint32_t bits = bits_of(ok, blk);
+                const int blk = wk * KB + kb, jb = jpos + 32 * blk;
+                const uint32_t bits = static_cast<uint32_t>((blk < 2 ? valid[S.value][0] : valid[S.value][PIDS - 1]) >> (32 * (blk & 1)));
+                const uint32_t sink = below(a.sinks - jb);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int kk = 8 * (r / 4) + 4 * hf + r % 4, j = jpos + 32 * blk + kk;
-                    const bool there = (bits >> kk) & 1;
+                for (int i = 0; i < QT; ++i) {
+                    // the block's keys that the lane's query attends to, from the lane's first on
+                    const uint32_t see = (bits & below(p_hi[i] - jb) & (~below(p_lo[i] - jb) | sink)) >> (4 * hf);
 #pragma unroll
-                    for (int i = 0; i < QT; ++i)
-                        if (!(there && j < p_hi[i] && (j >= p_lo[i] || j < a.sinks)))
-                            sv[kb][i][r] = -__builtin_inff();
+                    for (int r = 0; r < 16; ++r) {
+                        const uint32_t on = __builtin_amdgcn_sbfe(see, 8 * (r / 4) + r % 4, 1);  // all bits or none
+                        sv[kb][i][r] = __uint_as_float((__float_as_uint(sv[kb][i][r]) & on) | (0xff800000u & ~on));
+                    }
                 }
             }
         }
@@ -324,10 +361,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
         // O^T += V^T P^T
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            const int blk = wk * KB + kb;
-            const uint32_t bits = bits_of(ok, blk);
             if constexpr (EL == 2) {
-                const int j16 = lane & 15, cg = (lane >> 4) & 1;  // lane of a 16-lane group, column half
 #pragma unroll
                 for (int mm = 0; mm < 2; ++mm) {
                     bf16x8 pf[QT];
@@ -339,22 +373,11 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
                             f[e] = sv[kb][i][8 * mm + e];
                         pf[i] = to_bf16x8(f);
                     }
-                    const int vrow = 32 * blk + 16 * mm + 4 * hf + (j16 >> 2);
-                    u32x4 keep;
-                    if (MASKED.value) {
-                        const uint32_t lo = bits >> (16 * mm + 4 * hf), hi = lo >> 8;
-                        keep = u32x4{(lo & 1 ? 0xffffu : 0u) | (lo & 2 ? 0xffff0000u : 0u),
-                                     (lo & 4 ? 0xffffu : 0u) | (lo & 8 ? 0xffff0000u : 0u),
-                                     (hi & 1 ? 0xffffu : 0u) | (hi & 2 ? 0xffff0000u : 0u),
-                                     (hi & 4 ? 0xffffu : 0u) | (hi & 8 ? 0xffff0000u : 0u)};
-                    }
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        const int pc = (4 * d + 2 * cg + ((j16 & 3) >> 1)) ^ L::swz_v(j16 >> 2);
-                        const __bf16 *vr = reinterpret_cast<const __bf16 *>(vt + vrow * ROWB + pc * 16 + (j16 & 1) * 8);
-                        bf16x8 vf = cat(tr_read(vr), tr_read(vr + 8 * D));
-                        if (MASKED.value)
-                            vf = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, vf) & keep);
+                        constexpr int ROWS8 = 8 * ROWB;
+                        const bf16x8 vf = cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (32 * kb + 16 * mm) * ROWB])),
+                                              tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (32 * kb + 16 * mm) * ROWB + ROWS8])));
 #pragma unroll
                         for (int i = 0; i < QT; ++i)
                             o[i][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[i], o[i][d], 0, 0, 0);
@@ -363,13 +386,10 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
             } else {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int kk = 8 * (r / 4) + 4 * hf + r % 4;
-                    const float *vr = reinterpret_cast<const float *>(vt + (32 * blk + kk) * ROWB) + l32;
+                    const int kk = 32 * kb + 8 * (r / 4) + r % 4;
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        float vf = vr[32 * d];
-                        if (MASKED.value && !((bits >> kk) & 1))
-                            vf = 0.f;
+                        const float vf = *reinterpret_cast<const float *>(&VBUF(S)[voff[0] + kk * ROWB + 128 * d]);
 #pragma unroll
                         for (int i = 0; i < QT; ++i)
                             o[i][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, sv[kb][i][r], o[i][d], 0, 0, 0);
@@ -388,21 +408,26 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
             workgroup_lds_barrier<NST == 3 ? 2 * NC : 0>();
         else
             workgroup_lds_barrier<0>();
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < PIDS; ++i)
+            all = all && valid[S.value][i] == (TK < 64 ? 0xffffffffull : ~0ull);
+        if (!all) {  // the same for every wavefront
+#pragma unroll
+            for (int x = 0; x < C::TILE_BYTES / 16 / C::THREADS; ++x) {
+                const int piece = x * C::THREADS + threadIdx.x, row = piece / PPR;
+                if (!((valid[S.value][PIDS == 1 ? 0 : row >> 6] >> (row & 63)) & 1))
+                    *reinterpret_cast<uint4 *>(&VBUF(S)[piece * 16]) = make_uint4(0, 0, 0, 0);
+            }
+            workgroup_lds_barrier<63>();
+        }
         if (t + NST - 1 < t1)
             start(Int<(S.value + NST - 1) % NST>{}, t + NST - 1);
         const Where x = where(t);
         const int jpos = x.cached ? x.start : s.len + x.start;
-        if (active && jpos < w_himax && (jpos + TK > w_lomin || jpos < a.sinks)) {
-            bool all = true;
-#pragma unroll
-            for (int i = 0; i < PIDS; ++i)
-                all = all && valid[S.value][i] == (TK < 64 ? 0xffffffffull : ~0ull);
-            const bool whole = all && jpos + TK <= w_himin && (jpos >= w_lomax || jpos + TK <= a.sinks);
-            if (whole)
-                compute(S, Int<0>{}, jpos, valid[S.value]);
-            else
-                compute(S, Int<1>{}, jpos, valid[S.value]);
-        }
+        const bool whole = all && jpos + TK <= w_himin && (jpos >= w_lomax || jpos + TK <= a.sinks);
+        if (active && jpos < w_himax && (jpos + TK > w_lomin || jpos < a.sinks))
+            compute(S, whole, jpos);
     };
     if (t0 < t1) {
         load_ids(t0);
@@ -410,16 +435,13 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, int nrt, 
         if (NST == 3 && t0 + 1 < t1)
             start(Int<1>{}, t0 + 1);
     }
-    for (int t = t0; t < t1;) {
+    for (int t = t0; t < t1; t += NST) {
         step(Int<0>{}, t);
-        if (++t >= t1)
-            break;
-        step(Int<1>{}, t);
-        if (++t >= t1)
-            break;
+        if (t + 1 < t1)
+            step(Int<1>{}, t + 1);
         if constexpr (NST == 3) {
-            step(Int<2>{}, t);
-            ++t;
+            if (t + 2 < t1)
+                step(Int<2>{}, t + 2);
         }
     }
 #pragma unroll
@@ -564,7 +586,7 @@ auto by_rows(int64_t R, F f)
             return f.template operator()<T, D, 2, 1, 4, 128, 2, 1>();
         if (R <= 128)
             return f.template operator()<T, D, 2, 2, 2, 64, 2, (D == 64 ? 2 : 1)>();
-        return f.template operator()<T, D, 2, 4, 1, 64, 2, (D == 64 ? 2 : 1)>();
+        return f.template operator()<T, D, 1, 8, 1, 64, 2, (D == 64 ? 4 : 2)>();
     } else {
         if (R <= 32)
             return f.template operator()<T, D, 1, 1, (D == 64 ? 4 : 2), (D == 64 ? 128 : 64), 2, 1>();
@@ -581,16 +603,26 @@ struct PlanOf {
         AttnPlan p{};
         const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
         p.nrt = static_cast<int>((R + C::RT - 1) / C::RT);
-        // splits: enough workgroups to fill the GPU once, each with four tiles at least
+        // Ranges: the number whose rounds of workgroups take the fewest tiles in all, where a
+        // workgroup costs about six tiles beside its own, and a join about six more.
         const int64_t vis = a.window && static_cast<int64_t>(a.window) + a.block_len < a.max_len
                                 ? static_cast<int64_t>(a.window) + a.block_len + a.sinks
                                 : a.max_len;
-        const int64_t tiles = (vis + a.block_len + TK - 1) / TK, units = static_cast<int64_t>(a.batch) * a.KV * p.nrt;
+        const int64_t tiles = (vis + a.block_len + TK - 1) / TK, units = static_cast<int64_t>(a.batch) * a.KV;
         const int64_t slots = static_cast<int64_t>(device_cus()) * (4 * WPE / C::NW);
-        int64_t ns = slots / (units > 0 ? units : 1);
-        ns = ns < tiles / 4 ? ns : tiles / 4;
-        ns = ns < 1 ? 1 : ns < 128 ? ns : 128;
+        int64_t ns = 1, best = INT64_MAX;
+        for (int64_t x = 1; x <= 64 && x <= (tiles + 3) / 4; ++x) {
+            const int64_t cost = (units * p.nrt * x + slots - 1) / slots * ((tiles + x - 1) / x + 6) + (x > 1 ? 6 : 0);
+            if (cost < best)
+                best = cost, ns = x;
+        }
         p.nsplit = static_cast<int>(ns);
+        const int64_t all = units * ns;
+        p.sub = static_cast<int>(all >= 64 ? 1 : std::min<int64_t>(p.nrt, (64 + all - 1) / all));
+        p.nrt_sub = (p.nrt + p.sub - 1) / p.sub;
+        p.units = static_cast<int>(all * p.sub);
+        p.per_xcd = (p.units + 7) / 8;
+        p.rt_fast = p.nrt_sub <= 4;
         const int64_t rows = static_cast<int64_t>(a.batch) * a.KV * ns * R;
         p.ml_bytes = ns > 1 ? static_cast<size_t>((rows * 8 + 255) / 256 * 256) : 0;
         p.ws_bytes = ns > 1 ? p.ml_bytes + static_cast<size_t>(rows) * D * 4 : 0;
@@ -610,7 +642,7 @@ struct Launch {
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
         k_attn<T, D, QT, WM, WK, TK, NST, WPE>
-            <<<dim3(p.nrt, a.KV * p.nsplit, a.batch), C::THREADS, 0, st>>>(a, p.nrt, p.nsplit, part, ml);
+            <<<dim3(static_cast<unsigned>(8 * p.per_xcd) * p.nrt_sub), C::THREADS, 0, st>>>(a, p, part, ml);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.nsplit == 1)
             return e;
