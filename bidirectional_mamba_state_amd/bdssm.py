@@ -209,7 +209,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object, whose construction
+        # takes longer than the rest of a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -416,29 +418,40 @@ class DecodeGraph:
 
 
 # ------------------------------------------------- norms and attention around the Mamba layers
+# A decode step makes these calls for microseconds of GPU work, so their checks are plain
+# comparisons of what a tensor already holds.
 def _torch_dtype(dtype):
     import torch
     return torch.bfloat16 if dtype == BF16 else torch.float32
 
 
 def _expect(t, what, dtype, shape):
-    """A tensor argument whose sizes the library cannot see: its type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    """A tensor argument whose sizes the library cannot see: its type and shape (a tuple)."""
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
+def _expect_size(t, what, dtype, shape):
+    """Its type and number of elements: rows x width however the tensor splits them."""
+    if t.dtype != dtype or t.numel() != shape[0] * shape[1]:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
 def _rows(t, what, dtype, shape):
-    """(device pointer, elements between rows) of a tensor whose rows (all dimensions but the
-    first) are contiguous; the rows themselves may be slices of longer ones."""
+    """(device pointer, elements between rows) of a tensor of two or three dimensions whose rows
+    (all but the first) are contiguous; the rows themselves may be slices of longer ones."""
     if not getattr(t, "is_cuda", False):
         raise TypeError("bdssm takes device (CUDA/HIP) tensors only")
-    _expect(t, what, dtype, shape)
-    inner = 1
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and step != inner:
-            raise ValueError(f"{what}: rows must be contiguous")
-        inner *= size
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else inner
+    if t.dtype != dtype or t.shape != shape:
+        _expect(t, what, dtype, shape)
+    steps, width = t.stride(), shape[-1]
+    inside = steps[-1] == 1 or width == 1
+    if len(shape) == 3:
+        inside = inside and (steps[1] == width or shape[1] == 1)
+        width *= shape[1]
+    if not inside:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.data_ptr(), steps[0] if shape[0] > 1 else width
 
 
 def norm_dims(rows, width, dtype, groups=1, eps=1e-5, rows_per_stream=0, kind=NORM_RMS, x_dtype=None):
@@ -452,9 +465,8 @@ def gated_norm(nd, y, z, weight, out, norm_first=False, stream=None):
     dt = _torch_dtype(nd.dtype)
     shape = (nd.rows, nd.width)
     zp, zs = _rows(z, "z", dt, shape)
-    for t, what, ty in ((y, "y", _torch_dtype(nd.x_dtype)), (out, "out", dt)):
-        if t.dtype != ty or t.numel() != nd.rows * nd.width:
-            raise ValueError(f"{what}: expected {ty} {shape}, got {t.dtype} {tuple(t.shape)}")
+    _expect_size(y, "y", _torch_dtype(nd.x_dtype), shape)
+    _expect_size(out, "out", dt, shape)
     if weight is not None:
         _expect(weight, "weight", _torch_dtype(F32), shape[1:])
     _check(load().bdssm_gated_norm(ctypes.byref(nd), _ptr(y), zp, zs, _ptr(weight), int(norm_first), _ptr(out),
@@ -466,26 +478,36 @@ def residual_norm(nd, x, o, pre_w, x_out, u, post_w=None, gate=None, gain=None, 
     """bdssm_residual_norm: x, o, x_out, u [rows, width] contiguous (o, x_out or u may be None),
     post_w, pre_w [width] float32 or None, gate, gain, shift [streams, width] or None (slices of
     one projection's rows)."""
-    dt, xt, f32 = _torch_dtype(nd.dtype), _torch_dtype(nd.x_dtype), _torch_dtype(F32)
+    dt, xt = _torch_dtype(nd.dtype), _torch_dtype(nd.x_dtype)
     shape = (nd.rows, nd.width)
-    for t, what, ty in ((x, "x", xt), (o, "o", dt), (x_out, "x_out", xt), (u, "u", dt)):
-        if t is not None and (t.dtype != ty or t.numel() != nd.rows * nd.width):
-            raise ValueError(f"{what}: expected {ty} {shape}, got {t.dtype} {tuple(t.shape)}")
-    for t, what in ((post_w, "post_w"), (pre_w, "pre_w")):
-        if t is not None:
-            _expect(t, what, f32, shape[1:])
-    mods, strides = [], set()
-    for t, what in ((gate, "gate"), (gain, "gain"), (shift, "shift")):
-        if t is None:
-            mods.append(None)
-            continue
-        streams = -(-nd.rows // nd.rows_per_stream) if nd.rows_per_stream > 0 else 0
-        p, s = _rows(t, what, dt, (streams, nd.width))
-        mods.append(p)
-        strides.add(s)
-    if len(strides) > 1:
-        raise ValueError("gate, gain and shift must have one stride between streams")
-    r = Residual(_ptr(x), _ptr(o), _ptr(post_w), _ptr(pre_w), *mods, strides.pop() if strides else 0, res_scale)
+    _expect_size(x, "x", xt, shape)
+    if o is not None:
+        _expect_size(o, "o", dt, shape)
+    if x_out is not None:
+        _expect_size(x_out, "x_out", xt, shape)
+    if u is not None:
+        _expect_size(u, "u", dt, shape)
+    if post_w is not None:
+        _expect(post_w, "post_w", _torch_dtype(F32), shape[1:])
+    if pre_w is not None:
+        _expect(pre_w, "pre_w", _torch_dtype(F32), shape[1:])
+    gp = ap = sp = None
+    step = 0
+    if gate is not None or gain is not None or shift is not None:
+        per = (-(-nd.rows // nd.rows_per_stream) if nd.rows_per_stream > 0 else 0, nd.width)
+        steps = set()
+        if gate is not None:
+            gp, step = _rows(gate, "gate", dt, per)
+            steps.add(step)
+        if gain is not None:
+            ap, step = _rows(gain, "gain", dt, per)
+            steps.add(step)
+        if shift is not None:
+            sp, step = _rows(shift, "shift", dt, per)
+            steps.add(step)
+        if len(steps) > 1:
+            raise ValueError("gate, gain and shift must have one stride between streams")
+    r = Residual(_ptr(x), _ptr(o), _ptr(post_w), _ptr(pre_w), gp, ap, sp, step, res_scale)
     _check(load().bdssm_residual_norm(ctypes.byref(nd), ctypes.byref(r), _ptr(x_out), _ptr(u), _stream(stream)))
 
 
@@ -525,22 +547,28 @@ class KvCache:
     def set_lens(self, lens):
         """Another lengths tensor (the lens_out of an append)."""
         import torch
-        _expect(lens, "lens", torch.int32, tuple(self.lens.shape))
+        _expect(lens, "lens", torch.int32, self.lens.shape)
         self.ptrs.lens, self.lens = _ptr(lens), lens
 
 
 def _chunk(ad, block_len, q, k, v, starts):
     """A bdssm_attn_chunk of q [tokens, nheads, headdim], k, v [tokens, kv_heads, headdim] (rows
     may be slices of longer ones) and starts [batch + 1] int32 or None."""
-    dt = _torch_dtype(ad.dtype)
+    dt, D, kv = _torch_dtype(ad.dtype), ad.headdim, ad.kv_heads
     n = (q if q is not None else k).shape[0]
-    qp, qs = _rows(q, "q", dt, (n, ad.nheads, ad.headdim)) if q is not None else (None, 0)
-    kp, ks = _rows(k, "k", dt, (n, ad.kv_heads, ad.headdim)) if k is not None else (None, 0)
-    vp, vs = _rows(v, "v", dt, (n, ad.kv_heads, ad.headdim)) if v is not None else (None, 0)
+    qp = kp = vp = sp = None
+    qs = ks = vs = 0
+    if q is not None:
+        qp, qs = _rows(q, "q", dt, (n, ad.nheads, D))
+    if k is not None:
+        kp, ks = _rows(k, "k", dt, (n, kv, D))
+    if v is not None:
+        vp, vs = _rows(v, "v", dt, (n, kv, D))
     if starts is not None:
         import torch
         _expect(starts, "starts", torch.int32, (ad.batch + 1,))
-    return AttnChunk(qp, kp, vp, qs, ks, vs, n, _ptr(starts), block_len)
+        sp = _ptr(starts)
+    return AttnChunk(qp, kp, vp, qs, ks, vs, n, sp, block_len)
 
 
 def attn_step_workspace(ad, block_len, max_len, mask):

@@ -23,13 +23,14 @@
 // Copies. Keys and values go from the pages (or the chunk's rows) straight into LDS, 1 KB a
 // copy, each copy inside one page (a page holds 16 tokens or more, a copy 8 at most); the
 // 16-byte pieces of a row are permuted on the way (swz_k, swz_v) so that the operand reads are
-// free of bank conflicts. NST stages: NST - 1 tiles are in flight while one is computed.
+// free of bank conflicts. Two stages: the next tile is in flight while one is computed.
 //
 // Masks. Per tile a 64-bit mask says which keys exist, are held and are attended to by any row
 // of the workgroup; the values of the others (which may hold anything, NaN included) are cleared
 // in LDS before use. Scores are selected per element in tiles that some row of a wavefront does
 // not see whole; the other tiles skip that.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.h"
 #include "internal.h"
@@ -40,10 +41,12 @@ namespace bdssm {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kRaise = 8.f;  // see "Softmax" above
+
+#define kOnes (bf16x2{static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)})
 
 template <typename T, int D>
 struct Tile;
@@ -97,33 +100,33 @@ struct Int {
     static constexpr int value = N;
 };
 
-template <typename T, int D, int QT, int WM, int WK, int TK, int NST>
+template <typename T, int D, int QT, int WM, int WK, int TK>
 struct AttnCfg {
     static constexpr int NW = WM * WK, THREADS = 64 * NW, RT = 32 * QT * WM;
     static constexpr int TILE_BYTES = TK * Tile<T, D>::ROWB;
 };
 
-template <typename T, int D, int QT, int WM, int WK, int TK, int NST, int WPE>
-__global__ __launch_bounds__((AttnCfg<T, D, QT, WM, WK, TK, NST>::THREADS))
+template <typename T, int D, int QT, int WM, int WK, int TK, int WPE>
+__global__ __launch_bounds__((AttnCfg<T, D, QT, WM, WK, TK>::THREADS))
 __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan pl, float *part, float2 *part_ml)
 {
-    using C = AttnCfg<T, D, QT, WM, WK, TK, NST>;
+    using C = AttnCfg<T, D, QT, WM, WK, TK>;
     using L = Tile<T, D>;
     using Frag = typename L::Frag;
     constexpr int NW = C::NW, ROWB = L::ROWB, PPR = ROWB / 16;
     constexpr int RPC = 1024 / ROWB;                // rows of a copy
     constexpr int NC = C::TILE_BYTES / 1024 / NW;   // copies of a wavefront per tile, of K and of V
     constexpr int PIDS = (TK + 63) / 64;            // page number registers of a tile
-    constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile
+    constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile,
+    constexpr int KS = KB < 2 ? KB : 2;             // KS of them per softmax step
     constexpr int EL = sizeof(T);
-    static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0 && (NST == 2 || NST == 3), "tile shape");
+    static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0 , "tile shape");
 
     // one array per stage and operand, so that reads of one need not wait for copies into another
     __shared__ __attribute__((aligned(16))) char k0[C::TILE_BYTES], v0[C::TILE_BYTES], k1[C::TILE_BYTES], v1[C::TILE_BYTES];
-    __shared__ __attribute__((aligned(16))) char k2[NST == 3 ? C::TILE_BYTES : 16], v2[NST == 3 ? C::TILE_BYTES : 16];
     __shared__ float2 ml[WK > 1 ? NW * QT * 32 : 1];
-    auto KBUF = [&](auto S) -> char * { return S.value == 0 ? k0 : S.value == 1 ? k1 : k2; };
-    auto VBUF = [&](auto S) -> char * { return S.value == 0 ? v0 : S.value == 1 ? v1 : v2; };
+    auto KBUF = [&](auto S) -> char * { return S.value == 0 ? k0 : k1; };
+    auto VBUF = [&](auto S) -> char * { return S.value == 0 ? v0 : v1; };
 
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = w / WK, wk = w % WK, hf = lane >> 5, l32 = lane & 31;
@@ -170,28 +173,37 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const int nt = ns + nw + nc;
     const int per = (nt + nsplit - 1) / nsplit, t0 = split * per, t1 = t0 + per < nt ? t0 + per : nt;
 
-    struct Where {
+    struct Cursor {
+        int t, start;  // tile, and its first key: cached position or index into the chunk
         bool cached;
-        int start;  // cached position, or index into the chunk
     };
-    auto where = [&](int t) {
-        return t < ns        ? Where{true, t * TK}
-               : t < ns + nw ? Where{true, (w0 + t - ns) * TK}
-                             : Where{false, (c0 + t - ns - nw) * TK};
+    auto at = [&](int t) {
+        return t < ns        ? Cursor{t, t * TK, true}
+               : t < ns + nw ? Cursor{t, (w0 + t - ns) * TK, true}
+                             : Cursor{t, (c0 + t - ns - nw) * TK, false};
+    };
+    auto advance = [&](Cursor &x) {
+        ++x.t;
+        x.start += TK;
+        if (x.t == ns || x.t == ns + nw)
+            x = at(x.t);
     };
 
     // ---- copies
     const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    const int page = 1 << a.page_shift, last_key = s.len - 1;
-    int next_ids[PIDS] = {};
-    auto load_ids = [&](int t) {  // page numbers of a tile's keys, one key per lane
-        const Where x = where(t);
-        if (t < t1 && x.cached) {
-#pragma unroll
-            for (int i = 0; i < PIDS; ++i) {
-                const int j = x.start + 64 * i + lane;
-                next_ids[i] = table[(j < last_key ? j : last_key) >> a.page_shift];
-            }
+    const int page = 1 << a.page_shift, last_page = (s.len > 0 ? s.len - 1 : 0) >> a.page_shift;
+    // Page numbers: lane i holds the one of page pbase + i (pbase a multiple of 64, so that no
+    // tile straddles it), and in `ids_next` the one of 64 pages on.
+    int pbase = -1, ids = 0, ids_next = 0;
+    uint64_t held = 0;  // which of the 64 are pages of the pool
+    auto page_no = [&](int i) { return table[i < last_page ? i : last_page]; };
+    auto find_pages = [&](int start) {
+        const int p = (start >> a.page_shift) & ~63;
+        if (p != pbase) {
+            ids = pbase >= 0 && p == pbase + 64 ? ids_next : page_no(p + lane);
+            ids_next = page_no(p + 64 + lane);
+            pbase = p;
+            held = __ballot(static_cast<uint32_t>(ids) < static_cast<uint32_t>(a.num_pages));
         }
     };
     const int crow = lane / PPR, cslot = lane % PPR;  // row of a copy, LDS piece of that row
@@ -201,23 +213,25 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const char *vp = static_cast<const char *>(a.vp) + static_cast<int64_t>(kvh) * page_bytes;
     const char *ck = static_cast<const char *>(a.k) + (s.row0 * a.k_stride + static_cast<int64_t>(kvh) * D) * EL;
     const char *cv = static_cast<const char *>(a.v) + (s.row0 * a.v_stride + static_cast<int64_t>(kvh) * D) * EL;
-    uint64_t valid[NST][PIDS];  // per stage: the tile's keys that exist and that some row attends to
-    auto copy = [&](auto S, int t, const int (&ids)[PIDS]) {
-        const Where x = where(t);
+    uint64_t valid[2][PIDS];  // per stage: the tile's keys that exist and that some row attends to,
+    int jpos[2];              // and the position of its first key
+    auto copy = [&](auto S, const Cursor &x) {
+        jpos[S.value] = x.cached ? x.start : s.len + x.start;
+        if (x.cached)
+            find_pages(x.start);
 #pragma unroll
         for (int i = 0; i < PIDS; ++i) {
-            const int kk = 64 * i + lane, j = x.cached ? x.start + kk : s.len + x.start + kk;
-            const bool held = static_cast<uint32_t>(ids[i]) < static_cast<uint32_t>(a.num_pages);
-            const bool there = x.cached ? (j < s.len) & held : x.start + kk < n;
+            const int kk = 64 * i + lane, j = jpos[S.value] + kk;
+            const bool there = x.cached ? (j < s.len) & ((held >> ((j >> a.page_shift) & 63)) & 1) : j < end;
             valid[S.value][i] = __ballot((kk < TK) & there & (j < hi_max) & ((j >= lo_min) | (j < a.sinks)));
         }
         if (x.cached) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int row0 = (w + NW * c) * RPC, row = row0 + crow;
-                const uint32_t pg = __builtin_amdgcn_readlane(ids[RPC * NW * c / 64], row0 % 64);  // RPC NW divides 64
-                // a page that is not held: an empty range, nothing is read
-                const bool ok = pg < static_cast<uint32_t>(a.num_pages);
+                const int pi = ((x.start + row0) >> a.page_shift) & 63;
+                const uint32_t pg = __builtin_amdgcn_readlane(ids, pi);
+                const bool ok = (held >> pi) & 1;  // not held: an empty range, nothing is read
                 const uint64_t base = ok ? static_cast<uint64_t>(pg) * pool_step : 0;
                 const int off = ((x.start + row0) & (page - 1)) * ROWB + crow * ROWB;
                 copy_to_lds(buffer_range(kp + base, ok ? page_bytes : 0), KBUF(S) + row0 * ROWB,
@@ -239,15 +253,10 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             }
         }
     };
-    // the copies of tile t, and ahead of them (memory operations complete in order) the page
-    // numbers of the next tile
-    auto start = [&](auto S, int t) {
-        int ids[PIDS];
-#pragma unroll
-        for (int i = 0; i < PIDS; ++i)
-            ids[i] = next_ids[i];
-        load_ids(t + 1);
-        copy(S, t, ids);
+    Cursor nx = at(t0);  // the tile to be copied next
+    auto start = [&](auto S) {
+        copy(S, nx);
+        advance(nx);
     };
 
     // ---- queries: B operands, one row per lane
@@ -294,26 +303,30 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         asm volatile("" : "+v"(voff[0]));
     }
 
-    // ---- one tile, this wavefront's KB blocks of 32 keys
-    auto compute = [&](auto S, bool whole, int jpos) {
-        f32x16 sv[KB][QT];
+    // ---- a step: KS blocks of 32 keys of a tile, from this wavefront's block B0 on
+    f32x16 sv[KS][QT];                                                         // scores
+    typename std::conditional<EL == 2, bf16x8[2 * KS][QT], f32x16[KS][QT]>::type pw;  // weights, B operands
+    auto scores = [&](auto S, auto B0) {  // S^T = K Q^T
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < KS; ++kb) {
 #pragma unroll
             for (int i = 0; i < QT; ++i)
                 sv[kb][i] = f32x16{};
 #pragma unroll
             for (int st = 0; st < L::STEPS; ++st) {
-                const Frag kf = *reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * kb * ROWB]);
+                const Frag kf = *reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * (B0.value + kb) * ROWB]);
 #pragma unroll
                 for (int i = 0; i < QT; ++i)
                     sv[kb][i] = L::qk(kf, q[i][st], sv[kb][i]);
             }
         }
+    };
+    // the lane's queries over their keys (half of them; the other half's lane has the rest)
+    auto softmax = [&](auto S, auto B0, bool whole) {
         if (!whole) {
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const int blk = wk * KB + kb, jb = jpos + 32 * blk;
+            for (int kb = 0; kb < KS; ++kb) {
+                const int blk = wk * KB + B0.value + kb, jb = jpos[S.value] + 32 * blk;
                 const uint32_t bits = static_cast<uint32_t>((blk < 2 ? valid[S.value][0] : valid[S.value][PIDS - 1]) >> (32 * (blk & 1)));
                 const uint32_t sink = below(a.sinks - jb);
 #pragma unroll
@@ -328,12 +341,11 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
                 }
             }
         }
-        // softmax of the lane's query over its keys (half of them; the other half's lane has the rest)
 #pragma unroll
         for (int i = 0; i < QT; ++i) {
             float mx = sv[0][i][0];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < KS; ++kb)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     mx = fmaxf(mx, sv[kb][i][r]);
@@ -348,101 +360,125 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
                     o[i][d] *= f;
             }
             const float ref = m[i] == -__builtin_inff() ? 0.f : m[i];
-            float sum = 0.f;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+            for (int kb = 0; kb < KS; ++kb) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    sv[kb][i][r] = __builtin_amdgcn_exp2f(fmaf(sv[kb][i][r], sc, -ref));
-                    sum += sv[kb][i][r];
+                for (int x = 0; x < 2; ++x) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        f[e] = __builtin_amdgcn_exp2f(fmaf(sv[kb][i][8 * x + e], sc, -ref));
+                    if constexpr (EL == 2) {
+                        const bf16x8 h = to_bf16x8(f);
+                        pw[2 * kb + x][i] = h;
+                        // the sum is of the rounded weights, two per instruction
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            l[i] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{h[2 * e], h[2 * e + 1]}, kOnes, l[i], false);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            pw[kb][i][8 * x + e] = f[e];
+                            l[i] += f[e];
+                        }
+                    }
                 }
-            l[i] += sum;
+            }
         }
-        // O^T += V^T P^T
+    };
+    auto values = [&](auto S, auto B0) {  // O^T += V^T P^T
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = 0; kb < KS; ++kb) {
+            const int row = 32 * (B0.value + kb);
             if constexpr (EL == 2) {
 #pragma unroll
-                for (int mm = 0; mm < 2; ++mm) {
-                    bf16x8 pf[QT];
-#pragma unroll
-                    for (int i = 0; i < QT; ++i) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[e] = sv[kb][i][8 * mm + e];
-                        pf[i] = to_bf16x8(f);
-                    }
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        constexpr int ROWS8 = 8 * ROWB;
-                        const bf16x8 vf = cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (32 * kb + 16 * mm) * ROWB])),
-                                              tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (32 * kb + 16 * mm) * ROWB + ROWS8])));
+                        const bf16x8 vf =
+                            cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (row + 16 * x) * ROWB])),
+                                tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (row + 16 * x + 8) * ROWB])));
 #pragma unroll
                         for (int i = 0; i < QT; ++i)
-                            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[i], o[i][d], 0, 0, 0);
+                            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pw[2 * kb + x][i], o[i][d], 0, 0, 0);
                     }
-                }
             } else {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int kk = 32 * kb + 8 * (r / 4) + r % 4;
+                for (int r = 0; r < 16; ++r)
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        const float vf = *reinterpret_cast<const float *>(&VBUF(S)[voff[0] + kk * ROWB + 128 * d]);
+                        const float vf = *reinterpret_cast<const float *>(
+                            &VBUF(S)[voff[0] + (row + 8 * (r / 4) + r % 4) * ROWB + 128 * d]);
 #pragma unroll
                         for (int i = 0; i < QT; ++i)
-                            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, sv[kb][i][r], o[i][d], 0, 0, 0);
+                            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, pw[kb][i][r], o[i][d], 0, 0, 0);
                     }
-                }
             }
         }
     };
 
-    // ---- the loop over tiles: iteration t waits for tile t (its own copies, then everyone's),
-    // starts the copies of tile t + NST - 1 into the stage that was last read before the barrier,
-    // and computes
-    auto step = [&](auto S, int t) {
-        // at most the copies of the next NST - 2 tiles may be in flight
-        if (NST == 3 && t + 1 < t1)
-            workgroup_lds_barrier<NST == 3 ? 2 * NC : 0>();
-        else
-            workgroup_lds_barrier<0>();
+    // whether this wavefront has anything to do in the tile of stage S, and whether its rows see it whole
+    auto seen = [&](auto S) {
+        const int j0 = jpos[S.value];
+        return active && j0 < w_himax && (j0 + TK > w_lomin || j0 < a.sinks);
+    };
+    auto full = [&](auto S) {
         bool all = true;
 #pragma unroll
         for (int i = 0; i < PIDS; ++i)
             all = all && valid[S.value][i] == (TK < 64 ? 0xffffffffull : ~0ull);
-        if (!all) {  // the same for every wavefront
+        return all;
+    };
+    auto whole = [&](auto S) {
+        const int j0 = jpos[S.value];
+        return full(S) && j0 + TK <= w_himin && (j0 >= w_lomax || j0 + TK <= a.sinks);
+    };
+    auto clear_absent = [&](auto S) {  // this thread's share of the values no row attends to
 #pragma unroll
-            for (int x = 0; x < C::TILE_BYTES / 16 / C::THREADS; ++x) {
-                const int piece = x * C::THREADS + threadIdx.x, row = piece / PPR;
-                if (!((valid[S.value][PIDS == 1 ? 0 : row >> 6] >> (row & 63)) & 1))
-                    *reinterpret_cast<uint4 *>(&VBUF(S)[piece * 16]) = make_uint4(0, 0, 0, 0);
-            }
+        for (int x = 0; x < C::TILE_BYTES / 16 / C::THREADS; ++x) {
+            const int piece = x * C::THREADS + threadIdx.x, row = piece / PPR;
+            if (!((valid[S.value][PIDS == 1 ? 0 : row >> 6] >> (row & 63)) & 1))
+                *reinterpret_cast<uint4 *>(&VBUF(S)[piece * 16]) = make_uint4(0, 0, 0, 0);
+        }
+    };
+
+    // the queries' loads end here, not at their first use inside the loop, where the wait for them
+    // would be one for the copies in flight too
+#pragma unroll
+    for (int i = 0; i < QT; ++i)
+#pragma unroll
+        for (int st = 0; st < L::STEPS; ++st)
+            asm volatile("" : "+v"(q[i][st]));
+
+    // ---- the loop over tiles: iteration t waits for tile t (its own copies, then everyone's),
+    // starts the copies of the next tile into the stage that was last read before the barrier,
+    // and computes
+    auto step = [&](auto S, int t) {
+        workgroup_lds_barrier<0>();
+        if (!full(S)) {  // the same for every wavefront
+            clear_absent(S);
             workgroup_lds_barrier<63>();
         }
-        if (t + NST - 1 < t1)
-            start(Int<(S.value + NST - 1) % NST>{}, t + NST - 1);
-        const Where x = where(t);
-        const int jpos = x.cached ? x.start : s.len + x.start;
-        const bool whole = all && jpos + TK <= w_himin && (jpos >= w_lomax || jpos + TK <= a.sinks);
-        if (active && jpos < w_himax && (jpos + TK > w_lomin || jpos < a.sinks))
-            compute(S, whole, jpos);
+        if (t + 1 < t1)
+            start(Int<1 - S.value>{});
+        if (seen(S)) {
+            const bool wh = whole(S);
+            scores(S, Int<0>{});
+            softmax(S, Int<0>{}, wh);
+            values(S, Int<0>{});
+            if constexpr (KB > KS) {
+                scores(S, Int<KS>{});
+                softmax(S, Int<KS>{}, wh);
+                values(S, Int<KS>{});
+            }
+        }
     };
-    if (t0 < t1) {
-        load_ids(t0);
-        start(Int<0>{}, t0);
-        if (NST == 3 && t0 + 1 < t1)
-            start(Int<1>{}, t0 + 1);
-    }
-    for (int t = t0; t < t1; t += NST) {
+    if (t0 < t1)
+        start(Int<0>{});
+    for (int t = t0; t < t1; t += 2) {
         step(Int<0>{}, t);
         if (t + 1 < t1)
             step(Int<1>{}, t + 1);
-        if constexpr (NST == 3) {
-            if (t + 2 < t1)
-                step(Int<2>{}, t + 2);
-        }
     }
 #pragma unroll
     for (int i = 0; i < QT; ++i)
@@ -575,31 +611,31 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int nsplit, const
         *reinterpret_cast<f32x4 *>(out) = o;
 }
 
-// f(QT, WM, WK, TK, NST, WPE): the kernel shape for R rows per (stream, KV head).
+// f(QT, WM, WK, TK, WPE): the kernel shape for R rows per (stream, KV head).
 template <typename T, int D, typename F>
 auto by_rows(int64_t R, F f)
 {
     if constexpr (sizeof(T) == 2) {
         if (R <= 32)
-            return f.template operator()<T, D, 1, 1, 4, 128, 2, 1>();
+            return f.template operator()<T, D, 1, 1, 4, 128, 1>();
         if (R <= 64)
-            return f.template operator()<T, D, 2, 1, 4, 128, 2, 1>();
+            return f.template operator()<T, D, 2, 1, 4, 128, 1>();
         if (R <= 128)
-            return f.template operator()<T, D, 2, 2, 2, 64, 2, (D == 64 ? 2 : 1)>();
-        return f.template operator()<T, D, 1, 8, 1, 64, 2, (D == 64 ? 4 : 2)>();
+            return f.template operator()<T, D, 2, 2, 2, 64, (D == 64 ? 2 : 1)>();
+        return f.template operator()<T, D, 1, 8, 1, 64, (D == 64 ? 4 : 2)>();
     } else {
         if (R <= 32)
-            return f.template operator()<T, D, 1, 1, (D == 64 ? 4 : 2), (D == 64 ? 128 : 64), 2, 1>();
-        return f.template operator()<T, D, 1, 4, 1, (D == 64 ? 64 : 32), 2, (D == 64 ? 2 : 2)>();
+            return f.template operator()<T, D, 1, 1, (D == 64 ? 4 : 2), (D == 64 ? 128 : 64), 1>();
+        return f.template operator()<T, D, 1, 4, 1, (D == 64 ? 64 : 32), 2>();
     }
 }
 
 struct PlanOf {
     const AttnArgs &a;
-    template <typename T, int D, int QT, int WM, int WK, int TK, int NST, int WPE>
+    template <typename T, int D, int QT, int WM, int WK, int TK, int WPE>
     AttnPlan operator()() const
     {
-        using C = AttnCfg<T, D, QT, WM, WK, TK, NST>;
+        using C = AttnCfg<T, D, QT, WM, WK, TK>;
         AttnPlan p{};
         const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
         p.nrt = static_cast<int>((R + C::RT - 1) / C::RT);
@@ -635,13 +671,13 @@ struct Launch {
     const AttnPlan &p;
     void *ws;
     hipStream_t st;
-    template <typename T, int D, int QT, int WM, int WK, int TK, int NST, int WPE>
+    template <typename T, int D, int QT, int WM, int WK, int TK, int WPE>
     hipError_t operator()() const
     {
-        using C = AttnCfg<T, D, QT, WM, WK, TK, NST>;
+        using C = AttnCfg<T, D, QT, WM, WK, TK>;
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
-        k_attn<T, D, QT, WM, WK, TK, NST, WPE>
+        k_attn<T, D, QT, WM, WK, TK, WPE>
             <<<dim3(static_cast<unsigned>(8 * p.per_xcd) * p.nrt_sub), C::THREADS, 0, st>>>(a, p, part, ml);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.nsplit == 1)
