@@ -3,8 +3,8 @@
 //
 // Work split. The query heads of one KV head are packed with the tokens into rows, row
 // r = token * G + head-in-group, so that a tile of keys and values is read once for all of
-// them. A workgroup owns one (stream, KV head), a tile of RT = 32 QT WM rows and a range of the
-// keys that those rows attend to; a wavefront owns 32 QT rows and, where few rows leave
+// them. A workgroup owns one (stream, KV head), a tile of RT = 32 WM rows and a range of the
+// keys that those rows attend to; a wavefront owns 32 rows and, where few rows leave
 // wavefronts free (WK > 1), every WK-th part of each key tile. A long cache is cut into
 // `nsplit` ranges; partial results (unnormalized rows, maximum, sum) are joined by k_attn_join.
 //
@@ -30,7 +30,6 @@
 // in LDS before use. Scores are selected per element in tiles that some row of a wavefront does
 // not see whole; the other tiles skip that.
 #include <algorithm>
-#include <type_traits>
 
 #include "attn.h"
 #include "internal.h"
@@ -100,17 +99,17 @@ struct Int {
     static constexpr int value = N;
 };
 
-template <typename T, int D, int QT, int WM, int WK, int TK>
+template <typename T, int D, int WM, int WK, int TK>
 struct AttnCfg {
-    static constexpr int NW = WM * WK, THREADS = 64 * NW, RT = 32 * QT * WM;
+    static constexpr int NW = WM * WK, THREADS = 64 * NW, RT = 32 * WM;
     static constexpr int TILE_BYTES = TK * Tile<T, D>::ROWB;
 };
 
-template <typename T, int D, int QT, int WM, int WK, int TK, int WPE>
-__global__ __launch_bounds__((AttnCfg<T, D, QT, WM, WK, TK>::THREADS))
+template <typename T, int D, int WM, int WK, int TK, int WPE>
+__global__ __launch_bounds__((AttnCfg<T, D, WM, WK, TK>::THREADS))
 __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan pl, float *part, float2 *part_ml)
 {
-    using C = AttnCfg<T, D, QT, WM, WK, TK>;
+    using C = AttnCfg<T, D, WM, WK, TK>;
     using L = Tile<T, D>;
     using Frag = typename L::Frag;
     constexpr int NW = C::NW, ROWB = L::ROWB, PPR = ROWB / 16;
@@ -120,11 +119,12 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile,
     constexpr int KS = KB < 2 ? KB : 2;             // KS of them per softmax step
     constexpr int EL = sizeof(T);
-    static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0 , "tile shape");
+    constexpr uint64_t kAll = TK < 64 ? 0xffffffffull : ~0ull;  // a mask of keys with all of them
+    static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0, "tile shape");
 
     // one array per stage and operand, so that reads of one need not wait for copies into another
     __shared__ __attribute__((aligned(16))) char k0[C::TILE_BYTES], v0[C::TILE_BYTES], k1[C::TILE_BYTES], v1[C::TILE_BYTES];
-    __shared__ float2 ml[WK > 1 ? NW * QT * 32 : 1];
+    __shared__ float2 ml[WK > 1 ? NW * 32 : 1];
     auto KBUF = [&](auto S) -> char * { return S.value == 0 ? k0 : k1; };
     auto VBUF = [&](auto S) -> char * { return S.value == 0 ? v0 : v1; };
 
@@ -146,6 +146,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const int rows = s.n * G, r_first = rt * C::RT;
     if (r_first >= rows)
         return;
+    const int r_end = r_first + C::RT < rows ? r_first + C::RT : rows;
 
     // ---- what the workgroup's rows and this wavefront's rows attend to
     const int n = a.k ? s.n : 0, end = s.len + n;  // keys at positions [0, end)
@@ -156,11 +157,10 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         return h < end ? static_cast<int>(h) : end;
     };
     auto lo_of = [&](int p) { return a.window == 0 || p < a.window ? 0 : p - a.window + 1; };
-    const int r_last = (r_first + C::RT < rows ? r_first + C::RT : rows) - 1;
-    const int lo_min = lo_of(s.len + r_first / G), hi_max = hi_of(s.len + r_last / G);
-    const int wr0 = r_first + wm * 32 * QT;
-    const bool active = wr0 < rows;
-    const int wr1 = wr0 + 32 * QT - 1 < rows ? wr0 + 32 * QT - 1 : rows - 1;
+    const int lo_min = lo_of(s.len + r_first / G), hi_max = hi_of(s.len + (r_end - 1) / G);
+    const int wr0 = r_first + wm * 32;
+    const bool active = wr0 < r_end;
+    const int wr1 = wr0 + 31 < r_end ? wr0 + 31 : r_end - 1;
     const int w_pmin = s.len + wr0 / G, w_pmax = s.len + wr1 / G;
     const int w_himin = hi_of(w_pmin), w_himax = hi_of(w_pmax), w_lomax = lo_of(w_pmax), w_lomin = lo_of(w_pmin);
 
@@ -192,23 +192,26 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     // ---- copies
     const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
     const int page = 1 << a.page_shift, last_page = (s.len > 0 ? s.len - 1 : 0) >> a.page_shift;
-    // Page numbers: lane i holds the one of page pbase + i (pbase a multiple of 64, so that no
-    // tile straddles it), and in `ids_next` the one of 64 pages on.
-    int pbase = -1, ids = 0, ids_next = 0;
+    const int page_bytes = page * ROWB;
+    const uint32_t pool_step = static_cast<uint32_t>(a.KV * page_bytes);  // from page to page
+    // Pages: lane i holds the offset in its pool of page pbase + i (pbase a multiple of 64, so
+    // that no tile straddles it), and in `next` the number of the one 64 pages on.
+    int pbase = -1, next = 0;
+    uint32_t page_lo = 0, page_hi = 0;
     uint64_t held = 0;  // which of the 64 are pages of the pool
     auto page_no = [&](int i) { return table[i < last_page ? i : last_page]; };
     auto find_pages = [&](int start) {
         const int p = (start >> a.page_shift) & ~63;
         if (p != pbase) {
-            ids = pbase >= 0 && p == pbase + 64 ? ids_next : page_no(p + lane);
-            ids_next = page_no(p + 64 + lane);
+            const uint32_t id = pbase >= 0 && p == pbase + 64 ? next : page_no(p + lane);
+            next = page_no(p + 64 + lane);
             pbase = p;
-            held = __ballot(static_cast<uint32_t>(ids) < static_cast<uint32_t>(a.num_pages));
+            held = __ballot(id < static_cast<uint32_t>(a.num_pages));
+            const uint64_t off = static_cast<uint64_t>(id) * pool_step;
+            page_lo = static_cast<uint32_t>(off), page_hi = static_cast<uint32_t>(off >> 32);
         }
     };
     const int crow = lane / PPR, cslot = lane % PPR;  // row of a copy, LDS piece of that row
-    const int page_bytes = page * ROWB;
-    const uint32_t pool_step = static_cast<uint32_t>(a.KV * page_bytes);  // from page to page
     const char *kp = static_cast<const char *>(a.kp) + static_cast<int64_t>(kvh) * page_bytes;
     const char *vp = static_cast<const char *>(a.vp) + static_cast<int64_t>(kvh) * page_bytes;
     const char *ck = static_cast<const char *>(a.k) + (s.row0 * a.k_stride + static_cast<int64_t>(kvh) * D) * EL;
@@ -219,21 +222,27 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         jpos[S.value] = x.cached ? x.start : s.len + x.start;
         if (x.cached)
             find_pages(x.start);
+        if (x.cached && x.start + TK <= s.len && x.start >= lo_min && held == ~0ull) {
 #pragma unroll
-        for (int i = 0; i < PIDS; ++i) {
-            const int kk = 64 * i + lane, j = jpos[S.value] + kk;
-            const bool there = x.cached ? (j < s.len) & ((held >> ((j >> a.page_shift) & 63)) & 1) : j < end;
-            valid[S.value][i] = __ballot((kk < TK) & there & (j < hi_max) & ((j >= lo_min) | (j < a.sinks)));
+            for (int i = 0; i < PIDS; ++i)
+                valid[S.value][i] = kAll;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PIDS; ++i) {
+                const int kk = 64 * i + lane, j = jpos[S.value] + kk;
+                const bool there = x.cached ? (j < s.len) & ((held >> ((j >> a.page_shift) & 63)) & 1) : j < end;
+                valid[S.value][i] = __ballot((kk < TK) & there & (j < hi_max) & ((j >= lo_min) | (j < a.sinks)));
+            }
         }
         if (x.cached) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int row0 = (w + NW * c) * RPC, row = row0 + crow;
-                const int pi = ((x.start + row0) >> a.page_shift) & 63;
-                const uint32_t pg = __builtin_amdgcn_readlane(ids, pi);
+                const int pi = ((x.start + row0) >> a.page_shift) & 63, slot = (x.start + row0) & (page - 1);
                 const bool ok = (held >> pi) & 1;  // not held: an empty range, nothing is read
-                const uint64_t base = ok ? static_cast<uint64_t>(pg) * pool_step : 0;
-                const int off = ((x.start + row0) & (page - 1)) * ROWB + crow * ROWB;
+                const uint64_t base = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(page_hi, pi))) << 32 |
+                                      static_cast<uint32_t>(__builtin_amdgcn_readlane(page_lo, pi));
+                const int off = slot * ROWB + crow * ROWB;
                 copy_to_lds(buffer_range(kp + base, ok ? page_bytes : 0), KBUF(S) + row0 * ROWB,
                             off + (cslot ^ L::swz_k(row)) * 16);
                 copy_to_lds(buffer_range(vp + base, ok ? page_bytes : 0), VBUF(S) + row0 * ROWB,
@@ -260,25 +269,16 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     };
 
     // ---- queries: B operands, one row per lane
-    Frag q[QT][L::STEPS];
-    int p_hi[QT], p_lo[QT];  // the lane's query attends to keys in [p_lo, p_hi) and below a.sinks
+    Frag q[L::STEPS];
+    const int my_row = wr0 + l32 < r_end ? wr0 + l32 : r_end - 1, tok = my_row / G, head = kvh * G + my_row % G;
+    const int p_hi = hi_of(s.len + tok), p_lo = lo_of(s.len + tok);  // attends to [p_lo, p_hi) and below a.sinks
+    const T *q_row = static_cast<const T *>(a.q) + (s.row0 + tok) * a.q_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-        int r = wr0 + 32 * i + l32;
-        r = r < rows ? r : rows - 1;
-        const int tok = r / G, head = kvh * G + r % G;
-        p_hi[i] = hi_of(s.len + tok), p_lo[i] = lo_of(s.len + tok);
-        const T *qr = static_cast<const T *>(a.q) + (s.row0 + tok) * a.q_stride + static_cast<int64_t>(head) * D;
-#pragma unroll
-        for (int st = 0; st < L::STEPS; ++st)
-            q[i][st] = *reinterpret_cast<const Frag *>(qr + (2 * st + hf) * (16 / EL));
-    }
+    for (int st = 0; st < L::STEPS; ++st)
+        q[st] = *reinterpret_cast<const Frag *>(q_row + (2 * st + hf) * (16 / EL));
 
-    f32x16 o[QT][D / 32] = {};
-    float m[QT], l[QT];
-#pragma unroll
-    for (int i = 0; i < QT; ++i)
-        m[i] = -__builtin_inff(), l[i] = 0.f;
+    f32x16 o[D / 32] = {};
+    float m = -__builtin_inff(), l = 0.f;
     const float sc = a.scale * kLog2e;
 
     // ---- operand reads. Every lane offset is one opaque value, a single step from its array:
@@ -304,115 +304,93 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     }
 
     // ---- a step: KS blocks of 32 keys of a tile, from this wavefront's block B0 on
-    f32x16 sv[KS][QT];                                                         // scores
-    typename std::conditional<EL == 2, bf16x8[2 * KS][QT], f32x16[KS][QT]>::type pw;  // weights, B operands
+    f32x16 sv[KS];                        // scores
     auto scores = [&](auto S, auto B0) {  // S^T = K Q^T
 #pragma unroll
         for (int kb = 0; kb < KS; ++kb) {
+            sv[kb] = f32x16{};
 #pragma unroll
-            for (int i = 0; i < QT; ++i)
-                sv[kb][i] = f32x16{};
-#pragma unroll
-            for (int st = 0; st < L::STEPS; ++st) {
-                const Frag kf = *reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * (B0.value + kb) * ROWB]);
-#pragma unroll
-                for (int i = 0; i < QT; ++i)
-                    sv[kb][i] = L::qk(kf, q[i][st], sv[kb][i]);
-            }
+            for (int st = 0; st < L::STEPS; ++st)
+                sv[kb] = L::qk(*reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * (B0.value + kb) * ROWB]), q[st], sv[kb]);
         }
     };
-    // the lane's queries over their keys (half of them; the other half's lane has the rest)
-    auto softmax = [&](auto S, auto B0, bool whole) {
-        if (!whole) {
-#pragma unroll
-            for (int kb = 0; kb < KS; ++kb) {
-                const int blk = wk * KB + B0.value + kb, jb = jpos[S.value] + 32 * blk;
-                const uint32_t bits = static_cast<uint32_t>((blk < 2 ? valid[S.value][0] : valid[S.value][PIDS - 1]) >> (32 * (blk & 1)));
-                const uint32_t sink = below(a.sinks - jb);
-#pragma unroll
-                for (int i = 0; i < QT; ++i) {
-                    // the block's keys that the lane's query attends to, from the lane's first on
-                    const uint32_t see = (bits & below(p_hi[i] - jb) & (~below(p_lo[i] - jb) | sink)) >> (4 * hf);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const uint32_t on = __builtin_amdgcn_sbfe(see, 8 * (r / 4) + r % 4, 1);  // all bits or none
-                        sv[kb][i][r] = __uint_as_float((__float_as_uint(sv[kb][i][r]) & on) | (0xff800000u & ~on));
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < QT; ++i) {
-            float mx = sv[0][i][0];
-#pragma unroll
-            for (int kb = 0; kb < KS; ++kb)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    mx = fmaxf(mx, sv[kb][i][r]);
-            mx = half_max(mx) * sc;
-            if (__ballot(mx > m[i] + kRaise)) {
-                const float mn = fmaxf(m[i], mx);
-                const float f = m[i] == mn ? 1.f : __builtin_amdgcn_exp2f(m[i] - mn);  // equal infinities: 1
-                m[i] = mn;
-                l[i] *= f;
-#pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-                    o[i][d] *= f;
-            }
-            const float ref = m[i] == -__builtin_inff() ? 0.f : m[i];
-#pragma unroll
-            for (int kb = 0; kb < KS; ++kb) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = __builtin_amdgcn_exp2f(fmaf(sv[kb][i][8 * x + e], sc, -ref));
-                    if constexpr (EL == 2) {
-                        const bf16x8 h = to_bf16x8(f);
-                        pw[2 * kb + x][i] = h;
-                        // the sum is of the rounded weights, two per instruction
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            l[i] = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{h[2 * e], h[2 * e + 1]}, kOnes, l[i], false);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            pw[kb][i][8 * x + e] = f[e];
-                            l[i] += f[e];
-                        }
-                    }
-                }
-            }
-        }
-    };
-    auto values = [&](auto S, auto B0) {  // O^T += V^T P^T
+    auto hide = [&](auto S, auto B0) {  // scores of what the query does not attend to: -infinity
 #pragma unroll
         for (int kb = 0; kb < KS; ++kb) {
-            const int row = 32 * (B0.value + kb);
-            if constexpr (EL == 2) {
+            const int blk = wk * KB + B0.value + kb, jb = jpos[S.value] + 32 * blk;
+            const uint32_t bits = static_cast<uint32_t>((blk < 2 ? valid[S.value][0] : valid[S.value][PIDS - 1]) >> (32 * (blk & 1)));
+            // the block's keys that the query attends to, from the lane's first on
+            const uint32_t see = (bits & below(p_hi - jb) & (~below(p_lo - jb) | below(a.sinks - jb))) >> (4 * hf);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+            for (int r = 0; r < 16; ++r) {
+                const uint32_t on = __builtin_amdgcn_sbfe(see, 8 * (r / 4) + r % 4, 1);  // all bits or none
+                sv[kb][r] = __uint_as_float((__float_as_uint(sv[kb][r]) & on) | (0xff800000u & ~on));
+            }
+        }
+    };
+    // the query's new reference (a lane holds half of its keys; the other half's lane has the rest)
+    auto raise = [&]() {
+        float mx = sv[0][0];
+#pragma unroll
+        for (int kb = 0; kb < KS; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                mx = fmaxf(mx, sv[kb][r]);
+        mx = half_max(mx) * sc;
+        if (__ballot(mx > m + kRaise)) {
+            const float mn = fmaxf(m, mx);
+            const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);  // equal infinities: 1
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d)
+                o[d] *= f;
+        }
+    };
+    // weights, and O^T += V^T P^T one part of 16 keys behind them, so that a wavefront's products
+    // and exponentials overlap
+    auto weigh = [&](auto S, auto B0) {
+        constexpr int PARTS = 2 * KS;
+        const float ref = m == -__builtin_inff() ? 0.f : m;
+        float wt[PARTS][8];
+        bf16x8 wb[PARTS];
+#pragma unroll
+        for (int x = 0; x <= PARTS; ++x) {
+            if (x < PARTS) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    wt[x][e] = __builtin_amdgcn_exp2f(fmaf(sv[x / 2][8 * (x % 2) + e], sc, -ref));
+                if constexpr (EL == 2) {
+                    // the sum is of the rounded weights, two per instruction
+                    wb[x] = to_bf16x8(wt[x]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{wb[x][2 * e], wb[x][2 * e + 1]}, kOnes, l, false);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        l += wt[x][e];
+                }
+            }
+            if (x > 0) {
+                const int row = 32 * (B0.value + (x - 1) / 2) + 16 * ((x - 1) % 2);
+                if constexpr (EL == 2) {
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        const bf16x8 vf =
-                            cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (row + 16 * x) * ROWB])),
-                                tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (row + 16 * x + 8) * ROWB])));
-#pragma unroll
-                        for (int i = 0; i < QT; ++i)
-                            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pw[2 * kb + x][i], o[i][d], 0, 0, 0);
+                        const bf16x8 vf = cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + row * ROWB])),
+                                              tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (row + 8) * ROWB])));
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, wb[x - 1], o[d], 0, 0, 0);
                     }
-            } else {
+                } else {
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
+                    for (int e = 0; e < 8; ++e)
 #pragma unroll
-                    for (int d = 0; d < D / 32; ++d) {
-                        const float vf = *reinterpret_cast<const float *>(
-                            &VBUF(S)[voff[0] + (row + 8 * (r / 4) + r % 4) * ROWB + 128 * d]);
-#pragma unroll
-                        for (int i = 0; i < QT; ++i)
-                            o[i][d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, pw[kb][i][r], o[i][d], 0, 0, 0);
-                    }
+                        for (int d = 0; d < D / 32; ++d) {
+                            const int at = voff[0] + (row + 8 * (e / 4) + e % 4) * ROWB + 128 * d;
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(*reinterpret_cast<const float *>(&VBUF(S)[at]),
+                                                                        wt[x - 1][e], o[d], 0, 0, 0);
+                        }
+                }
             }
         }
     };
@@ -426,7 +404,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         bool all = true;
 #pragma unroll
         for (int i = 0; i < PIDS; ++i)
-            all = all && valid[S.value][i] == (TK < 64 ? 0xffffffffull : ~0ull);
+            all = all && valid[S.value][i] == kAll;
         return all;
     };
     auto whole = [&](auto S) {
@@ -445,10 +423,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     // the queries' loads end here, not at their first use inside the loop, where the wait for them
     // would be one for the copies in flight too
 #pragma unroll
-    for (int i = 0; i < QT; ++i)
-#pragma unroll
-        for (int st = 0; st < L::STEPS; ++st)
-            asm volatile("" : "+v"(q[i][st]));
+    for (int st = 0; st < L::STEPS; ++st)
+        asm volatile("" : "+v"(q[st]));
 
     // ---- the loop over tiles: iteration t waits for tile t (its own copies, then everyone's),
     // starts the copies of the next tile into the stage that was last read before the barrier,
@@ -464,12 +440,16 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         if (seen(S)) {
             const bool wh = whole(S);
             scores(S, Int<0>{});
-            softmax(S, Int<0>{}, wh);
-            values(S, Int<0>{});
+            if (!wh)
+                hide(S, Int<0>{});
+            raise();
+            weigh(S, Int<0>{});
             if constexpr (KB > KS) {
                 scores(S, Int<KS>{});
-                softmax(S, Int<KS>{}, wh);
-                values(S, Int<KS>{});
+                if (!wh)
+                    hide(S, Int<KS>{});
+                raise();
+                weigh(S, Int<KS>{});
             }
         }
     };
@@ -480,128 +460,148 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         if (t + 1 < t1)
             step(Int<1>{}, t + 1);
     }
-#pragma unroll
-    for (int i = 0; i < QT; ++i)
-        l[i] = half_sum(l[i]);
+    l = half_sum(l);
 
     // ---- wavefronts that shared the rows: join in LDS, in wavefront order
     if constexpr (WK > 1) {
         constexpr int UNIT = 32 * D * 4, PER = C::TILE_BYTES / UNIT;  // bytes of 32 rows; units per array
-        static_assert((WK - 1) * WM * QT <= 4 * PER, "the stages hold the partial rows");
-        auto unit = [&](int u) -> float * {
-            char *arr = u / PER == 0 ? k0 : u / PER == 1 ? v0 : u / PER == 2 ? k1 : v1;
-            return reinterpret_cast<float *>(arr + (u % PER) * UNIT);
+        static_assert((WK - 1) * WM <= 4 * PER, "the stages hold the partial rows");
+        auto unit = [&](int x) {  // the x-th other wavefront's rows
+            const int i = (x - 1) * WM + wm;
+            char *arr = i / PER == 0 ? k0 : i / PER == 1 ? v0 : i / PER == 2 ? k1 : v1;
+            return reinterpret_cast<f32x4 *>(arr + (i % PER) * UNIT);
         };
         __syncthreads();
+        if (hf == 0)
+            ml[w * 32 + l32] = make_float2(m, l);
+        if (wk > 0) {
+            f32x4 *to = unit(wk);
 #pragma unroll
-        for (int i = 0; i < QT; ++i) {
-            if (hf == 0)
-                ml[(w * QT + i) * 32 + l32] = make_float2(m[i], l[i]);
-            if (wk > 0) {
-                f32x4 *u = reinterpret_cast<f32x4 *>(unit(((wk - 1) * WM + wm) * QT + i));
+            for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        u[(d * 4 + r) * 64 + lane] = f32x4{o[i][d][4 * r], o[i][d][4 * r + 1], o[i][d][4 * r + 2], o[i][d][4 * r + 3]};
-            }
+                for (int r = 0; r < 4; ++r)
+                    to[(d * 4 + r) * 64 + lane] = f32x4{o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]};
         }
         __syncthreads();
         if (wk > 0)
             return;
+        const float own = m;
 #pragma unroll
-        for (int i = 0; i < QT; ++i) {
-            float mt = m[i];
+        for (int x = 1; x < WK; ++x)
+            m = fmaxf(m, ml[(w + x) * 32 + l32].x);
+        const float f0 = own == m ? 1.f : __builtin_amdgcn_exp2f(own - m);
+        l *= f0;
 #pragma unroll
-            for (int x = 1; x < WK; ++x)
-                mt = fmaxf(mt, ml[((w + x) * QT + i) * 32 + l32].x);
-            const float f0 = m[i] == mt ? 1.f : __builtin_amdgcn_exp2f(m[i] - mt);
-            l[i] *= f0;
+        for (int d = 0; d < D / 32; ++d)
+            o[d] *= f0;
+#pragma unroll
+        for (int x = 1; x < WK; ++x) {
+            const float2 v = ml[(w + x) * 32 + l32];
+            const float f = v.x == m ? 1.f : __builtin_amdgcn_exp2f(v.x - m);
+            l = fmaf(v.y, f, l);
+            const f32x4 *from = unit(x);
 #pragma unroll
             for (int d = 0; d < D / 32; ++d)
-                o[i][d] *= f0;
 #pragma unroll
-            for (int x = 1; x < WK; ++x) {
-                const float2 om = ml[((w + x) * QT + i) * 32 + l32];
-                const float f = om.x == mt ? 1.f : __builtin_amdgcn_exp2f(om.x - mt);
-                l[i] = fmaf(om.y, f, l[i]);
-                const f32x4 *u = reinterpret_cast<const f32x4 *>(unit(((x - 1) * WM + wm) * QT + i));
+                for (int r = 0; r < 4; ++r) {
+                    const f32x4 ov = from[(d * 4 + r) * 64 + lane];
 #pragma unroll
-                for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const f32x4 ov = u[(d * 4 + r) * 64 + lane];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[i][d][4 * r + e] = fmaf(ov[e], f, o[i][d][4 * r + e]);
-                    }
-            }
-            m[i] = mt;
+                    for (int e = 0; e < 4; ++e)
+                        o[d][4 * r + e] = fmaf(ov[e], f, o[d][4 * r + e]);
+                }
         }
     }
 
     // ---- rows out: normalized, or partial with their maximum and sum
-    const int64_t R = static_cast<int64_t>(a.block_len) * G;
+    if (wr0 + l32 >= r_end)
+        return;
+    if (nsplit == 1) {
+        const float inv = l > 0.f ? 1.f / l : l;  // nothing attended to: 0; NaN stays
+        T *out = static_cast<T *>(a.out) + ((s.row0 + tok) * a.H + head) * D + 4 * hf;
 #pragma unroll
-    for (int i = 0; i < QT; ++i) {
-        const int r = wr0 + 32 * i + l32;
-        if (r >= rows)
-            continue;
-        if (nsplit == 1) {
-            const float inv = l[i] > 0.f ? 1.f / l[i] : l[i];  // nothing attended to: 0; NaN stays
-            T *out = static_cast<T *>(a.out) + ((s.row0 + r / G) * a.H + kvh * G + r % G) * D + 4 * hf;
+        for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d)
+            for (int x = 0; x < 4; ++x) {
+                const f32x4 ov = f32x4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]} * inv;
+                if constexpr (EL == 2)
+                    *reinterpret_cast<bf16x4 *>(out + 32 * d + 8 * x) = __builtin_convertvector(ov, bf16x4);
+                else
+                    *reinterpret_cast<f32x4 *>(out + 32 * d + 8 * x) = ov;
+            }
+    } else {
+        const int64_t R = static_cast<int64_t>(a.block_len) * G;
+        const int64_t at = ((static_cast<int64_t>(b) * a.KV + kvh) * nsplit + split) * R + wr0 + l32;
+        if (hf == 0)
+            part_ml[at] = make_float2(m, l);
+        float *out = part + at * D + 4 * hf;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const f32x4 ov = f32x4{o[i][d][4 * x], o[i][d][4 * x + 1], o[i][d][4 * x + 2], o[i][d][4 * x + 3]} * inv;
-                    if constexpr (EL == 2)
-                        *reinterpret_cast<bf16x4 *>(out + 32 * d + 8 * x) = __builtin_convertvector(ov, bf16x4);
-                    else
-                        *reinterpret_cast<f32x4 *>(out + 32 * d + 8 * x) = ov;
-                }
-        } else {
-            const int64_t u = ((static_cast<int64_t>(b) * a.KV + kvh) * nsplit + split) * R + r;
-            if (hf == 0)
-                part_ml[u] = make_float2(m[i], l[i]);
-            float *out = part + u * D + 4 * hf;
+        for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-            for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    *reinterpret_cast<f32x4 *>(out + 32 * d + 8 * x) =
-                        f32x4{o[i][d][4 * x], o[i][d][4 * x + 1], o[i][d][4 * x + 2], o[i][d][4 * x + 3]};
-        }
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<f32x4 *>(out + 32 * d + 8 * x) =
+                    f32x4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]};
     }
 }
 
-// Joins the partial rows of a split cache: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
-// in split order. D/4 lanes hold a row; a split whose range was empty (sum 0) is not read.
-template <typename T, int D>
+// Joins the partial rows of a split cache: out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.
+// D/4 lanes hold a row, and GROUPS such groups of a workgroup take every GROUPS-th range, joined
+// in LDS in group order: many ranges of few rows are read by as many lanes as few of many.
+// A range that attended to nothing (sum 0) counts with weight 0: its rows were written.
+template <typename T, int D, int GROUPS>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int nsplit, const float *part, const float2 *part_ml)
 {
-    constexpr int LPR = D / 4;
+    constexpr int LPR = D / 4, RPW = 256 / LPR / GROUPS;  // lanes of a row, rows of a workgroup
+    __shared__ f32x4 so[GROUPS > 1 ? 256 : 1];
+    __shared__ float2 sml[GROUPS > 1 ? 256 : 1];
     const int b = blockIdx.z, kvh = blockIdx.y, G = a.H / a.KV;
-    const int r = blockIdx.x * (256 / LPR) + threadIdx.x / LPR, c = 4 * (threadIdx.x % LPR);
+    const int lr = threadIdx.x % LPR, g = threadIdx.x / LPR % GROUPS;
+    const int r = blockIdx.x * RPW + threadIdx.x / LPR / GROUPS, c = 4 * lr;
     const AttnStream s = attn_stream(a, b);
-    if (r >= s.n * G)
-        return;
+    const bool mine = r < s.n * G;
     const int64_t R = static_cast<int64_t>(a.block_len) * G, u0 = (static_cast<int64_t>(b) * a.KV + kvh) * nsplit * R + r;
-    float M = -__builtin_inff();
-    for (int x = 0; x < nsplit; ++x)
-        M = fmaxf(M, part_ml[u0 + x * R].x);
-    float l = 0.f;
+    float M = -__builtin_inff(), l = 0.f;
     f32x4 o = {};
+    if (mine) {
 #pragma unroll 4
-    for (int x = 0; x < nsplit; ++x) {
-        const float2 v = part_ml[u0 + x * R];
-        const f32x4 ov = *reinterpret_cast<const f32x4 *>(part + (u0 + x * R) * D + c);
-        const float f = v.x == M ? 1.f : __builtin_amdgcn_exp2f(v.x - M);
-        l = fmaf(v.y, f, l);
+        for (int x = g; x < nsplit; x += GROUPS)
+            M = fmaxf(M, part_ml[u0 + x * R].x);
+#pragma unroll 4
+        for (int x = g; x < nsplit; x += GROUPS) {
+            const float2 v = part_ml[u0 + x * R];
+            const f32x4 ov = *reinterpret_cast<const f32x4 *>(part + (u0 + x * R) * D + c);
+            const float f = v.x == M ? 1.f : __builtin_amdgcn_exp2f(v.x - M);
+            l = fmaf(v.y, f, l);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o[e] = fmaf(ov[e], f, o[e]);
+            for (int e = 0; e < 4; ++e)
+                o[e] = fmaf(ov[e], f, o[e]);
+        }
     }
+    if constexpr (GROUPS > 1) {
+        so[threadIdx.x] = o;
+        sml[threadIdx.x] = make_float2(M, l);
+        __syncthreads();
+        if (g > 0)
+            return;
+        const int first = threadIdx.x;
+#pragma unroll
+        for (int x = 1; x < GROUPS; ++x)
+            M = fmaxf(M, sml[first + x * LPR].x);
+        const float f0 = sml[first].x == M ? 1.f : __builtin_amdgcn_exp2f(sml[first].x - M);
+        l *= f0;
+        o *= f0;
+#pragma unroll
+        for (int x = 1; x < GROUPS; ++x) {
+            const float2 v = sml[first + x * LPR];
+            const f32x4 ov = so[first + x * LPR];
+            const float f = v.x == M ? 1.f : __builtin_amdgcn_exp2f(v.x - M);
+            l = fmaf(v.y, f, l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = fmaf(ov[e], f, o[e]);
+        }
+    }
+    if (!mine)
+        return;
     const float inv = l > 0.f ? 1.f / l : l;
     o *= inv;
     T *out = static_cast<T *>(a.out) + ((s.row0 + r / G) * a.H + kvh * G + r % G) * D + c;
@@ -611,44 +611,60 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int nsplit, const
         *reinterpret_cast<f32x4 *>(out) = o;
 }
 
-// f(QT, WM, WK, TK, WPE): the kernel shape for R rows per (stream, KV head).
+template <typename T, int D, int GROUPS>
+void join(const AttnArgs &a, int nsplit, const float *part, const float2 *ml, hipStream_t st)
+{
+    constexpr int RPW = 256 / (D / 4) / GROUPS;
+    const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
+    k_attn_join<T, D, GROUPS><<<dim3(static_cast<unsigned>((R + RPW - 1) / RPW), a.KV, a.batch), 256, 0, st>>>(a, nsplit, part, ml);
+}
+
+// f(WM, WK, TK, WPE): the kernel shape for R rows per (stream, KV head).
 template <typename T, int D, typename F>
 auto by_rows(int64_t R, F f)
 {
     if constexpr (sizeof(T) == 2) {
         if (R <= 32)
-            return f.template operator()<T, D, 1, 1, 4, 128, 1>();
+            return f.template operator()<T, D, 1, 4, 128, (D == 64 ? 2 : 1)>();
         if (R <= 64)
-            return f.template operator()<T, D, 2, 1, 4, 128, 1>();
-        if (R <= 128)
-            return f.template operator()<T, D, 2, 2, 2, 64, (D == 64 ? 2 : 1)>();
-        return f.template operator()<T, D, 1, 8, 1, 64, (D == 64 ? 4 : 2)>();
+            return f.template operator()<T, D, 2, 2, 64, (D == 64 ? 3 : 2)>();
+        return f.template operator()<T, D, 8, 1, 64, (D == 64 ? 4 : 2)>();
     } else {
         if (R <= 32)
-            return f.template operator()<T, D, 1, 1, (D == 64 ? 4 : 2), (D == 64 ? 128 : 64), 1>();
-        return f.template operator()<T, D, 1, 4, 1, (D == 64 ? 64 : 32), 2>();
+            return f.template operator()<T, D, 1, (D == 64 ? 4 : 2), (D == 64 ? 128 : 64), 1>();
+        return f.template operator()<T, D, 4, 1, (D == 64 ? 64 : 32), 2>();
     }
 }
 
 struct PlanOf {
     const AttnArgs &a;
-    template <typename T, int D, int QT, int WM, int WK, int TK, int WPE>
+    template <typename T, int D, int WM, int WK, int TK, int WPE>
     AttnPlan operator()() const
     {
-        using C = AttnCfg<T, D, QT, WM, WK, TK>;
+        using C = AttnCfg<T, D, WM, WK, TK>;
         AttnPlan p{};
         const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
         p.nrt = static_cast<int>((R + C::RT - 1) / C::RT);
-        // Ranges: the number whose rounds of workgroups take the fewest tiles in all, where a
-        // workgroup costs about six tiles beside its own, and a join about six more.
-        const int64_t vis = a.window && static_cast<int64_t>(a.window) + a.block_len < a.max_len
-                                ? static_cast<int64_t>(a.window) + a.block_len + a.sinks
-                                : a.max_len;
-        const int64_t tiles = (vis + a.block_len + TK - 1) / TK, units = static_cast<int64_t>(a.batch) * a.KV;
-        const int64_t slots = static_cast<int64_t>(device_cus()) * (4 * WPE / C::NW);
+        // Ranges: the number that makes the workgroups take the fewest tiles in all, one after
+        // the other on a place of the GPU. A workgroup costs some tiles beside its own (its
+        // start and first copies, and where the keys are split its partial rows). Rows in order
+        // of their blocks come longest first and end together; without an order the rounds are
+        // whole and, streams being of unequal lengths, the last one ends half a workgroup late.
+        // float32 products fill a CU's matrix cores with one workgroup, so two that share one
+        // take turns; with bf16 all that fit run together. Measured at 64 streams of 16-32K
+        // tokens, 768 rows: 1495 us whole, 1250 in four ranges; at 8,192 ordered rows of 5 heads:
+        // 1020 us whole, 1077 in two.
+        const bool f32 = sizeof(T) == 4;
+        const int64_t span = std::min<int64_t>(a.block_len, (C::RT + a.H / a.KV - 1) / (a.H / a.KV));
+        int64_t keys = static_cast<int64_t>(a.max_len) + a.block_len;  // of one row tile, at most
+        if (a.window)
+            keys = std::min(keys, static_cast<int64_t>(a.window) + a.sinks + span + TK);
+        const int64_t tiles = (keys + TK - 1) / TK, units = static_cast<int64_t>(a.batch) * a.KV;
+        const int64_t slots = static_cast<int64_t>(device_cus()) * (f32 ? 1 : 4 * WPE / C::NW);
         int64_t ns = 1, best = INT64_MAX;
         for (int64_t x = 1; x <= 64 && x <= (tiles + 3) / 4; ++x) {
-            const int64_t cost = (units * p.nrt * x + slots - 1) / slots * ((tiles + x - 1) / x + 6) + (x > 1 ? 6 : 0);
+            const int64_t per = (tiles + x - 1) / x, all = units * p.nrt * x, each = per + 6 + (x > 1 ? 2 * C::RT / TK : 0);
+            const int64_t cost = a.block && all > slots ? 2 * all * each / slots : 2 * ((all + slots - 1) / slots) * each + per;
             if (cost < best)
                 best = cost, ns = x;
         }
@@ -671,20 +687,21 @@ struct Launch {
     const AttnPlan &p;
     void *ws;
     hipStream_t st;
-    template <typename T, int D, int QT, int WM, int WK, int TK, int WPE>
+    template <typename T, int D, int WM, int WK, int TK, int WPE>
     hipError_t operator()() const
     {
-        using C = AttnCfg<T, D, QT, WM, WK, TK>;
+        using C = AttnCfg<T, D, WM, WK, TK>;
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
-        k_attn<T, D, QT, WM, WK, TK, WPE>
+        k_attn<T, D, WM, WK, TK, WPE>
             <<<dim3(static_cast<unsigned>(8 * p.per_xcd) * p.nrt_sub), C::THREADS, 0, st>>>(a, p, part, ml);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.nsplit == 1)
             return e;
-        const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
-        k_attn_join<T, D><<<dim3(static_cast<unsigned>((R * (D / 4) + 255) / 256), a.KV, a.batch), 256, 0, st>>>(
-            a, p.nsplit, part, ml);
+        if (p.nsplit < 8)
+            join<T, D, 1>(a, p.nsplit, part, ml, st);
+        else
+            join<T, D, 8>(a, p.nsplit, part, ml, st);
         return hipGetLastError();
     }
 };

@@ -11,9 +11,11 @@
 //              u = norm(r) pre_w gain_b + shift_b
 //
 // LPR lanes hold a row, VPT pieces of 8 channels each: 16 lanes to 256 channels, a wavefront
-// to 2048 (no barrier: the sums stay in one wavefront), a workgroup of four to 16384. Rows of
-// any length and alignment take the same path: a global load of 16 bytes needs no more than
-// its element's alignment on gfx950, and the last piece of a row is read by elements.
+// to 2048 (no barrier: the sums stay in one wavefront), a workgroup of four to 16384. Where there
+// are too few rows to fill the GPU anyway, a workgroup takes any row of more than 512 channels:
+// the time is then one row's chain of loads and sums. Rows of any length and alignment take the
+// same path: a global load of 16 bytes needs no more than its element's alignment on gfx950,
+// and the last piece of a row is read by elements.
 #include <limits.h>
 
 #include "bdssm.h"
@@ -45,19 +47,19 @@ struct ResidualArgs {
     int layer;
 };
 
+// Eight channels as loaded (one 16-byte piece of bf16, two of float32; the element's alignment
+// is enough), and their float32 values. Kept apart so that a load can be issued early and
+// waited for where its values are used.
 template <typename T>
-struct Piece;  // eight channels as one or two 16-byte pieces with the element's alignment
+struct Piece;
 
 template <>
 struct Piece<__bf16> {
     typedef __bf16 v __attribute__((ext_vector_type(8), aligned(2)));
-    static __device__ __forceinline__ void load(const __bf16 *p, float (&f)[8])
-    {
-        const bf16x8 a = *reinterpret_cast<const v *>(p);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f[k] = static_cast<float>(a[k]);
-    }
+    bf16x8 a;
+    __device__ __forceinline__ void load(const __bf16 *p) { a = *reinterpret_cast<const v *>(p); }
+    __device__ __forceinline__ void set(int k, __bf16 x) { a[k] = x; }
+    __device__ __forceinline__ float get(int k) const { return static_cast<float>(a[k]); }
     static __device__ __forceinline__ void store(__bf16 *p, const float (&f)[8])
     {
         *reinterpret_cast<v *>(p) = to_bf16x8(f);
@@ -67,13 +69,14 @@ struct Piece<__bf16> {
 template <>
 struct Piece<float> {
     typedef float v __attribute__((ext_vector_type(4), aligned(4)));
-    static __device__ __forceinline__ void load(const float *p, float (&f)[8])
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const float *p)
     {
-        const f32x4 a = *reinterpret_cast<const v *>(p), b = *reinterpret_cast<const v *>(p + 4);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            f[k] = a[k], f[4 + k] = b[k];
+        a = *reinterpret_cast<const v *>(p);
+        b = *reinterpret_cast<const v *>(p + 4);
     }
+    __device__ __forceinline__ void set(int k, float x) { k < 4 ? a[k & 3] = x : b[k & 3] = x; }
+    __device__ __forceinline__ float get(int k) const { return k < 4 ? a[k & 3] : b[k & 3]; }
     static __device__ __forceinline__ void store(float *p, const float (&f)[8])
     {
         *reinterpret_cast<v *>(p) = f32x4{f[0], f[1], f[2], f[3]};
@@ -83,14 +86,18 @@ struct Piece<float> {
 
 // channels c .. c+7 of a row of n; channels past the end read as zero, their stores are dropped
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int c, int n, float (&f)[8])
+__device__ __forceinline__ void load8(const T *p, int c, int n, Piece<T> &f)
 {
     if (c + 8 <= n) {
-        Piece<T>::load(p + c, f);
+        f.load(p + c);
     } else {
+        f = Piece<T>{};
+        if (c < n) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f[k] = c + k < n ? static_cast<float>(p[c + k]) : 0.f;
+            for (int k = 0; k < 7; ++k)
+                if (c + k < n)
+                    f.set(k, p[c + k]);
+        }
     }
 }
 
@@ -99,9 +106,9 @@ __device__ __forceinline__ void store8(T *p, int c, int n, const float (&f)[8])
 {
     if (c + 8 <= n) {
         Piece<T>::store(p + c, f);
-    } else {
+    } else if (c < n) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 7; ++k)
             if (c + k < n)
                 p[c + k] = static_cast<T>(f[k]);
     }
@@ -165,11 +172,60 @@ __device__ __forceinline__ void normalize(float (&x)[VPT][8], int lane, int n, f
             x[i][k] *= r;
 }
 
+// Whether weights and modulation are loaded ahead of the sums: in the shapes that few rows take.
+// With many rows other rows' loads fill that time, and the registers cost more (65,536 rows of
+// 1,024: 95 us, 118 us with everything ahead).
+template <int LPR, int VPT>
+constexpr bool kAhead = LPR == 256 && VPT <= 2;
+
 // Workgroup number in a grid folded over y (the threads along x have to fit 32 bits)
 __device__ __forceinline__ int64_t block_index()
 {
     return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
 }
+
+// The lane's VPT pieces of a row of n channels, loaded ahead (AHEAD) or when they are used.
+template <typename T, int LPR, int VPT, bool AHEAD>
+struct RowLoad {
+    const T *p;
+    int lane, n;
+    Piece<T> f[AHEAD ? VPT : 1];
+    __device__ __forceinline__ RowLoad(const T *row, int lane_, int n_) : p(row), lane(lane_), n(n_)
+    {
+        if (AHEAD && p) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                load8(p, (lane + i * LPR) * 8, n, f[AHEAD ? i : 0]);
+        }
+    }
+    __device__ __forceinline__ void get(int i, float (&x)[8])
+    {
+        if (!AHEAD)
+            load8(p, (lane + i * LPR) * 8, n, f[0]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = f[AHEAD ? i : 0].get(k);
+    }
+    __device__ __forceinline__ void values(float (&x)[VPT][8])
+    {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            get(i, x[i]);
+    }
+    __device__ __forceinline__ void multiply(float (&x)[VPT][8])  // x *= the row; nothing where it is NULL
+    {
+        if (!p)
+            return;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float w[8];
+            get(i, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[i][k] *= w[k];
+        }
+    }
+};
 
 template <typename Ty, typename T, int LPR, int VPT, bool NORM_FIRST>
 __global__ __launch_bounds__(256) void k_gated_norm(GatedArgs a)
@@ -184,13 +240,12 @@ __global__ __launch_bounds__(256) void k_gated_norm(GatedArgs a)
     const int n = a.width / a.groups, c0 = static_cast<int>(unit % a.groups) * n;
     const Ty *y = static_cast<const Ty *>(a.y) + row * a.width + c0;
     const T *z = static_cast<const T *>(a.z) + row * a.z_stride + c0;
+    RowLoad<Ty, LPR, VPT, true> y_row(y, lane, n);
+    RowLoad<T, LPR, VPT, true> z_row(z, lane, n);
+    RowLoad<float, LPR, VPT, kAhead<LPR, VPT>> weight(a.w ? a.w + c0 : nullptr, lane, n);
     float v[VPT][8], g[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = (lane + i * LPR) * 8;
-        load8(y, c, n, v[i]);
-        load8(z, c, n, g[i]);
-    }
+    y_row.values(v);
+    z_row.values(g);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -200,23 +255,16 @@ __global__ __launch_bounds__(256) void k_gated_norm(GatedArgs a)
                 v[i][k] *= g[i][k];
         }
     normalize<LPR, VPT>(v, lane, n, a.eps, 0, red);
+    weight.multiply(v);
     T *out = static_cast<T *>(a.out) + row * a.width + c0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (lane + i * LPR) * 8;
-        float w[8];
-        if (a.w) {
-            load8(a.w + c0, c, n, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[i][k] *= w[k];
-        }
         if (NORM_FIRST) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 v[i][k] *= g[i][k];
         }
-        store8(out, c, n, v[i]);
+        store8(out, (lane + i * LPR) * 8, n, v[i]);
     }
 }
 
@@ -231,37 +279,22 @@ __global__ __launch_bounds__(256) void k_residual_norm(ResidualArgs a)
         return;
     const Tx *x = static_cast<const Tx *>(a.x) + row * n;
     const int64_t mod = static_cast<int64_t>(static_cast<int>(row) / a.rps) * a.mod_stride;
+    auto modulation = [&](const void *p) { return p ? static_cast<const T *>(p) + mod : nullptr; };
+    constexpr bool AHEAD = kAhead<LPR, VPT>;
+    RowLoad<Tx, LPR, VPT, true> x_row(x, lane, n);
+    RowLoad<T, LPR, VPT, true> o_row(a.o ? static_cast<const T *>(a.o) + row * n : nullptr, lane, n);
+    RowLoad<float, LPR, VPT, AHEAD> post_w(a.post_w, lane, n), pre_w(a.pre_w, lane, n);
+    RowLoad<T, LPR, VPT, AHEAD> gate(modulation(a.gate), lane, n), gain(modulation(a.gain), lane, n),
+        shift(modulation(a.shift), lane, n);
     float r[VPT][8], t[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        load8(x, (lane + i * LPR) * 8, n, r[i]);
+    x_row.values(r);
     if (a.o) {
-        const T *o = static_cast<const T *>(a.o) + row * n;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            load8(o, (lane + i * LPR) * 8, n, t[i]);
+        o_row.values(t);
         if (a.post_w) {
             normalize<LPR, VPT>(t, lane, n, a.eps, a.layer, red);
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                float w[8];
-                load8(a.post_w, (lane + i * LPR) * 8, n, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    t[i][k] *= w[k];
-            }
+            post_w.multiply(t);
         }
-        if (a.gate) {
-            const T *g = static_cast<const T *>(a.gate) + mod;
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                float w[8];
-                load8(g, (lane + i * LPR) * 8, n, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    t[i][k] *= w[k];
-            }
-        }
+        gate.multiply(t);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
@@ -277,38 +310,32 @@ __global__ __launch_bounds__(256) void k_residual_norm(ResidualArgs a)
     if (!a.u)
         return;
     normalize<LPR, VPT>(r, lane, n, a.eps, a.layer, red + 8);
+    pre_w.multiply(r);
+    gain.multiply(r);
     T *u = static_cast<T *>(a.u) + row * n;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int c = (lane + i * LPR) * 8;
-        float w[8];
-        if (a.pre_w) {
-            load8(a.pre_w, c, n, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                r[i][k] *= w[k];
-        }
-        if (a.gain) {
-            load8(static_cast<const T *>(a.gain) + mod, c, n, w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                r[i][k] *= w[k];
-        }
         if (a.shift) {
-            load8(static_cast<const T *>(a.shift) + mod, c, n, w);
+            float w[8];
+            shift.get(i, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 r[i][k] += w[k];
         }
-        store8(u, c, n, r[i]);
+        store8(u, (lane + i * LPR) * 8, n, r[i]);
     }
 }
 
-// f<LPR, VPT>(): the lanes of a row and the pieces of a lane for n channels
+// f<LPR, VPT>(): the lanes of a row and the pieces of a lane for `rows` rows of n channels. Few
+// rows: less than two workgroups per CU with a row each (32 rows of 2,048: 4.9 us with a
+// wavefront per row, 3.9 us with a workgroup).
 template <typename F>
-hipError_t by_width(int n, F f)
+hipError_t by_width(int64_t rows, int n, F f)
 {
     const int pieces = (n + 7) / 8;
+    const bool few = rows <= 2 * device_cus();
+    if (few && pieces > 64 && pieces <= 256)
+        return f.template operator()<256, 1>();
     if (pieces <= 32)
         return f.template operator()<16, 2>();
     if (pieces <= 64)
@@ -419,10 +446,10 @@ extern "C" bdssm_status bdssm_gated_norm(const bdssm_norm_dims *dims, const void
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int w = dims->width / dims->groups;
     if (dims->dtype == BDSSM_F32)
-        return launched(by_width(w, LaunchGated<float, float>{a, norm_first != 0, st}));
+        return launched(by_width(dims->rows * dims->groups, w, LaunchGated<float, float>{a, norm_first != 0, st}));
     if (dims->x_dtype == BDSSM_F32)
-        return launched(by_width(w, LaunchGated<float, __bf16>{a, norm_first != 0, st}));
-    return launched(by_width(w, LaunchGated<__bf16, __bf16>{a, norm_first != 0, st}));
+        return launched(by_width(dims->rows * dims->groups, w, LaunchGated<float, __bf16>{a, norm_first != 0, st}));
+    return launched(by_width(dims->rows * dims->groups, w, LaunchGated<__bf16, __bf16>{a, norm_first != 0, st}));
 }
 
 extern "C" bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const bdssm_residual *r, void *x_out, void *u,
@@ -464,8 +491,8 @@ extern "C" bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const b
                          r->res_scale, dims->kind == BDSSM_NORM_LAYER};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (dims->dtype == BDSSM_F32)
-        return launched(by_width(dims->width, LaunchResidual<float, float>{a, st}));
+        return launched(by_width(dims->rows, dims->width, LaunchResidual<float, float>{a, st}));
     if (dims->x_dtype == BDSSM_F32)
-        return launched(by_width(dims->width, LaunchResidual<float, __bf16>{a, st}));
-    return launched(by_width(dims->width, LaunchResidual<__bf16, __bf16>{a, st}));
+        return launched(by_width(dims->rows, dims->width, LaunchResidual<float, __bf16>{a, st}));
+    return launched(by_width(dims->rows, dims->width, LaunchResidual<__bf16, __bf16>{a, st}));
 }
