@@ -8,6 +8,29 @@
 
 namespace bdssm {
 
+// Division of n in [0, 2^31) by a number the host knows: with k = ceil(log2 d) and
+// mul = floor(2^(31+k) / d) + 1, floor(n mul / 2^(31+k)) = floor(n / d), since mul d exceeds
+// 2^(31+k) by at most d <= 2^k, which n < 2^31 cannot make a whole 2^(31+k). A kernel's start
+// has some twenty divisions, and each would take thirty instructions.
+struct Divisor {
+    uint32_t d = 1, mul = 0, shift = 0;  // mul 0: d is 1
+    Divisor() = default;
+    explicit Divisor(int64_t by) : d(static_cast<uint32_t>(by))
+    {
+        if (d <= 1)
+            return;
+        const int k = 32 - __builtin_clz(d - 1);
+        mul = static_cast<uint32_t>((uint64_t{1} << (31 + k)) / d + 1);
+        shift = k - 1;
+    }
+    __host__ __device__ __forceinline__ int operator()(int n) const
+    {
+        const uint32_t u = static_cast<uint32_t>(n);
+        return static_cast<int>(mul ? static_cast<uint32_t>(static_cast<uint64_t>(u) * mul >> 32) >> shift : u);
+    }
+    __host__ __device__ __forceinline__ int rest(int n) const { return n - (*this)(n) * static_cast<int>(d); }
+};
+
 struct AttnArgs {
     const void *q, *k, *v;  // chunk rows; k, v NULL: no keys of its own
     int64_t q_stride, k_stride, v_stride;
@@ -20,6 +43,7 @@ struct AttnArgs {
     int batch, H, KV, page_shift;
     float scale;
     int block, window, sinks;
+    Divisor by_block, by_group;  // block (1 where it is 0), H / KV
     void *out;
 };
 
@@ -58,6 +82,7 @@ struct AttnPlan {
     int nrt, nsplit;                  // row tiles per (stream, KV head); ranges of its keys
     int sub, nrt_sub, units, per_xcd; // parts per unit, row tiles per part, parts, parts per XCD
     int rt_fast;
+    Divisor by_inner, by_units, by_kv, by_split;  // nrt_sub or per_xcd, units / sub, KV, nsplit
     size_t ml_bytes, ws_bytes;        // workspace: maxima and sums first, then rows (0 unless split)
 };
 

@@ -179,6 +179,8 @@ extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm
     if (a.batch == 0 || a.block_len == 0 || a.tokens == 0)
         return BDSSM_OK;
     a.scale = mask->scale, a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
+    a.by_block = Divisor(mask->block > 0 ? mask->block : 1);
+    a.by_group = Divisor(dims->nheads / dims->kv_heads);
     a.out = out;
     if (!rows_fit(a))
         return BDSSM_ERR_UNSUPPORTED;

@@ -132,16 +132,20 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const int wm = w / WK, wk = w % WK, hf = lane >> 5, l32 = lane & 31;
 
     // ---- this workgroup's part, row tile and unit (see AttnPlan)
-    const int nsplit = pl.nsplit, wid = blockIdx.x >> 3;
-    const int part_no = (pl.rt_fast ? wid / pl.nrt_sub : wid % pl.per_xcd) * 8 + (blockIdx.x & 7);
+    const int nsplit = pl.nsplit, wid = blockIdx.x >> 3, outer = pl.by_inner(wid), inner = wid - outer * static_cast<int>(pl.by_inner.d);
+    const int part_no = (pl.rt_fast ? outer : inner) * 8 + (blockIdx.x & 7);
     if (part_no >= pl.units)
         return;
-    const int per_sub = pl.units / pl.sub, u = part_no % per_sub;
-    const int rt_up = (pl.rt_fast ? wid % pl.nrt_sub : wid / pl.per_xcd) * pl.sub + part_no / per_sub;
+    const int which = pl.by_units(part_no), u = pl.by_units.rest(part_no);
+    const int rt_up = (pl.rt_fast ? inner : outer) * pl.sub + which;
     if (rt_up >= pl.nrt)
         return;
     const int rt = a.block ? pl.nrt - 1 - rt_up : rt_up;  // ordered: the longest ranges first
-    const int kvh = u % a.KV, split = u / a.KV % nsplit, b = u / a.KV / nsplit, G = a.H / a.KV;
+    const int uk = pl.by_kv(u), kvh = pl.by_kv.rest(u), b = pl.by_split(uk), split = pl.by_split.rest(uk);
+    const int G = static_cast<int>(a.by_group.d);
+    const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    auto page_no = [&](int i) { return a.max_pages > 0 ? table[i < a.max_pages ? i : a.max_pages - 1] : -1; };
+    const int first_pages[2] = {page_no(lane), page_no(64 + lane)};
     const AttnStream s = attn_stream(a, b);
     const int rows = s.n * G, r_first = rt * C::RT;
     if (r_first >= rows)
@@ -153,15 +157,15 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     auto hi_of = [&](int p) {  // keys below this are in p's block or before it
         if (a.block == 0)
             return end;
-        const int64_t h = static_cast<int64_t>(p / a.block + 1) * a.block;
+        const int64_t h = static_cast<int64_t>(a.by_block(p) + 1) * a.block;
         return h < end ? static_cast<int>(h) : end;
     };
     auto lo_of = [&](int p) { return a.window == 0 || p < a.window ? 0 : p - a.window + 1; };
-    const int lo_min = lo_of(s.len + r_first / G), hi_max = hi_of(s.len + (r_end - 1) / G);
+    const int lo_min = lo_of(s.len + a.by_group(r_first)), hi_max = hi_of(s.len + a.by_group(r_end - 1));
     const int wr0 = r_first + wm * 32;
     const bool active = wr0 < r_end;
     const int wr1 = wr0 + 31 < r_end ? wr0 + 31 : r_end - 1;
-    const int w_pmin = s.len + wr0 / G, w_pmax = s.len + wr1 / G;
+    const int w_pmin = s.len + a.by_group(wr0), w_pmax = s.len + a.by_group(wr1);
     const int w_himin = hi_of(w_pmin), w_himax = hi_of(w_pmax), w_lomax = lo_of(w_pmax), w_lomin = lo_of(w_pmin);
 
     // ---- tiles: sinks outside the window, the cached window, the chunk's own keys
@@ -171,7 +175,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const int c_lo = a.sinks > s.len || lo_min <= s.len ? 0 : lo_min - s.len, c_hi = hi_max - s.len;  // c_hi may be <= c_lo
     const int c0 = c_lo / TK, nc = n > 0 && c_hi > c_lo ? (c_hi + TK - 1) / TK - c0 : 0;
     const int nt = ns + nw + nc;
-    const int per = (nt + nsplit - 1) / nsplit, t0 = split * per, t1 = t0 + per < nt ? t0 + per : nt;
+    const int per = pl.by_split(nt + nsplit - 1), t0 = split * per, t1 = t0 + per < nt ? t0 + per : nt;
 
     struct Cursor {
         int t, start;  // tile, and its first key: cached position or index into the chunk
@@ -190,23 +194,24 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     };
 
     // ---- copies
-    const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
     const int page = 1 << a.page_shift, last_page = (s.len > 0 ? s.len - 1 : 0) >> a.page_shift;
     const int page_bytes = page * ROWB;
     const uint32_t pool_step = static_cast<uint32_t>(a.KV * page_bytes);  // from page to page
     // Pages: lane i holds the offset in its pool of page pbase + i (pbase a multiple of 64, so
-    // that no tile straddles it), and in `next` the number of the one 64 pages on.
-    int pbase = -1, next = 0;
+    // that no tile straddles it), and in `next` the number of the one 64 pages on. The first 64
+    // are loaded along with the stream's length, before it is known whether they are needed.
+    int pbase = -1, next = first_pages[1];
     uint32_t page_lo = 0, page_hi = 0;
-    uint64_t held = 0;  // which of the 64 are pages of the pool
-    auto page_no = [&](int i) { return table[i < last_page ? i : last_page]; };
+    uint64_t held = 0, whole_pages = 0;  // which of the 64 are pages of the pool; or past the stream's last
     auto find_pages = [&](int start) {
         const int p = (start >> a.page_shift) & ~63;
         if (p != pbase) {
-            const uint32_t id = pbase >= 0 && p == pbase + 64 ? next : page_no(p + lane);
-            next = page_no(p + 64 + lane);
+            const uint32_t id = p == 0 ? first_pages[0] : p == pbase + 64 ? next : page_no(p + lane);
+            if (p != 0)
+                next = page_no(p + 64 + lane);
             pbase = p;
             held = __ballot(id < static_cast<uint32_t>(a.num_pages));
+            whole_pages = held | __ballot(p + lane > last_page);
             const uint64_t off = static_cast<uint64_t>(id) * pool_step;
             page_lo = static_cast<uint32_t>(off), page_hi = static_cast<uint32_t>(off >> 32);
         }
@@ -222,7 +227,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         jpos[S.value] = x.cached ? x.start : s.len + x.start;
         if (x.cached)
             find_pages(x.start);
-        if (x.cached && x.start + TK <= s.len && x.start >= lo_min && held == ~0ull) {
+        if (x.cached && x.start + TK <= s.len && x.start >= lo_min && whole_pages == ~0ull) {
 #pragma unroll
             for (int i = 0; i < PIDS; ++i)
                 valid[S.value][i] = kAll;
@@ -270,7 +275,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
 
     // ---- queries: B operands, one row per lane
     Frag q[L::STEPS];
-    const int my_row = wr0 + l32 < r_end ? wr0 + l32 : r_end - 1, tok = my_row / G, head = kvh * G + my_row % G;
+    const int my_row = wr0 + l32 < r_end ? wr0 + l32 : r_end - 1, tok = a.by_group(my_row), head = kvh * G + my_row - tok * G;
     const int p_hi = hi_of(s.len + tok), p_lo = lo_of(s.len + tok);  // attends to [p_lo, p_hi) and below a.sinks
     const T *q_row = static_cast<const T *>(a.q) + (s.row0 + tok) * a.q_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
@@ -553,7 +558,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int nsplit, const
     constexpr int LPR = D / 4, RPW = 256 / LPR / GROUPS;  // lanes of a row, rows of a workgroup
     __shared__ f32x4 so[GROUPS > 1 ? 256 : 1];
     __shared__ float2 sml[GROUPS > 1 ? 256 : 1];
-    const int b = blockIdx.z, kvh = blockIdx.y, G = a.H / a.KV;
+    const int b = blockIdx.z, kvh = blockIdx.y, G = static_cast<int>(a.by_group.d);
     const int lr = threadIdx.x % LPR, g = threadIdx.x / LPR % GROUPS;
     const int r = blockIdx.x * RPW + threadIdx.x / LPR / GROUPS, c = 4 * lr;
     const AttnStream s = attn_stream(a, b);
@@ -604,7 +609,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, int nsplit, const
         return;
     const float inv = l > 0.f ? 1.f / l : l;
     o *= inv;
-    T *out = static_cast<T *>(a.out) + ((s.row0 + r / G) * a.H + kvh * G + r % G) * D + c;
+    const int tok = a.by_group(r);
+    T *out = static_cast<T *>(a.out) + ((s.row0 + tok) * a.H + kvh * G + r - tok * G) * D + c;
     if constexpr (sizeof(T) == 2)
         *reinterpret_cast<bf16x4 *>(out) = __builtin_convertvector(o, bf16x4);
     else
@@ -675,6 +681,10 @@ struct PlanOf {
         p.units = static_cast<int>(all * p.sub);
         p.per_xcd = (p.units + 7) / 8;
         p.rt_fast = p.nrt_sub <= 4;
+        p.by_inner = Divisor(p.rt_fast ? p.nrt_sub : p.per_xcd);
+        p.by_units = Divisor(all);
+        p.by_kv = Divisor(a.KV);
+        p.by_split = Divisor(ns);
         const int64_t rows = static_cast<int64_t>(a.batch) * a.KV * ns * R;
         p.ml_bytes = ns > 1 ? static_cast<size_t>((rows * 8 + 255) / 256 * 256) : 0;
         p.ws_bytes = ns > 1 ? p.ml_bytes + static_cast<size_t>(rows) * D * 4 : 0;
