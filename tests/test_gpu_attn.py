@@ -230,6 +230,52 @@ def test_large_scores(dtype):
     c.check("large")
 
 
+@pytest.mark.parametrize("dtype,D,block", [(BF16, 64, 0), (BF16, 64, 32), (BF16, 128, 1), (F32, 64, 0), (F32, 128, 32)])
+def test_many_streams_of_several_row_tiles(dtype, D, block):
+    """Streams of 0 to 3 row tiles in one launch, split and not, some without chunk tokens."""
+    _case(f"row tiles {dtype} {D} {block}")
+    Case([700, 0, 333, 64, 129, 31, 640, 5, 256], [100, 90, 0, 1, 64, 33, 43, 86, 7], H=12, KV=2, D=D, dtype=dtype,
+         page=32, block=block, ragged=True).check("row tiles")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("block", [0, 1])
+def test_one_kv_head_of_many_rows(dtype, block):
+    """One unit with many row tiles: they are dealt to all XCDs."""
+    _case(f"many rows {dtype} {block}")
+    Case([40], [650], H=4, KV=1, dtype=dtype, block=block).check("many rows")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (900, 4), (2500, 40)])
+def test_more_than_64_pages(dtype, window, sinks):
+    """Page numbers are kept 64 at a time: caches of more, windows that start past the first 64,
+    pages not held among the second 64."""
+    _case(f"pages {dtype} {window}")
+    Case([3000, 1024, 1040], [20, 20, 20], H=4, KV=2, dtype=dtype, page=16, window=window, sinks=sinks).check("pages")
+    Case([3000], [3], H=2, KV=1, dtype=dtype, page=16, window=window, sinks=sinks,
+         drop=[(0, i) for i in range(150, 160)]).check("pages not held")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ranges_that_see_nothing(dtype):
+    """A long cache split over workgroups where whole ranges hold no page: they join with weight 0,
+    and where no range sees anything the result is zero."""
+    import torch
+    _case("empty ranges")
+    Case([5000], [2], H=2, KV=1, dtype=dtype, page=64, own_keys=False, drop=[(0, i) for i in range(0, 50)]).check("some")
+    c = Case([5000], [2], H=2, KV=1, dtype=dtype, page=64, own_keys=False, drop=[(0, i) for i in range(0, 79)])
+    assert torch.count_nonzero(c.run()) == 0
+
+
+def test_launch_plans_keep_their_results():
+    """The same stream alone (few units: its keys split, its row tiles dealt to all XCDs) and among
+    others (many units): the same attention within the bound of each."""
+    _case("alone and among others")
+    for lens, counts in (([900], [60]), ([900] * 9, [60] * 9)):
+        Case(lens, counts, H=16, KV=2, page=32).check(f"{len(lens)} streams")
+
+
 def test_repeatable_streams_and_extra_rows():
     import torch
     c = Case([1000, 37], [16, 16], H=8, KV=2)
