@@ -45,8 +45,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kRaise = 8.f;  // see "Softmax" above
 
-#define kOnes (bf16x2{static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)})
-
 template <typename T, int D>
 struct Tile;
 
@@ -91,6 +89,13 @@ __device__ __forceinline__ float half_sum(float v)
     return __uint_as_float(s[0]) + __uint_as_float(s[1]);
 }
 
+// s plus weights 2e and 2e + 1 of w
+__device__ __forceinline__ float add_pair(bf16x8 w, int e, float s)
+{
+    const bf16x2 ones = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
+    return __builtin_amdgcn_fdot2_f32_bf16(bf16x2{w[2 * e], w[2 * e + 1]}, ones, s, false);
+}
+
 // the n lowest bits, for any n
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -116,8 +121,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     constexpr int RPC = 1024 / ROWB;                // rows of a copy
     constexpr int NC = C::TILE_BYTES / 1024 / NW;   // copies of a wavefront per tile, of K and of V
     constexpr int PIDS = (TK + 63) / 64;            // page number registers of a tile
-    constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile,
-    constexpr int KS = KB < 2 ? KB : 2;             // KS of them per softmax step
+    constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile
     constexpr int EL = sizeof(T);
     constexpr uint64_t kAll = TK < 64 ? 0xffffffffull : ~0ull;  // a mask of keys with all of them
     static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0, "tile shape");
@@ -308,21 +312,21 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         asm volatile("" : "+v"(voff[0]));
     }
 
-    // ---- a step: KS blocks of 32 keys of a tile, from this wavefront's block B0 on
-    f32x16 sv[KS];                        // scores
-    auto scores = [&](auto S, auto B0) {  // S^T = K Q^T
+    // ---- one tile: this wavefront's KB blocks of 32 keys
+    f32x16 sv[KB];               // scores
+    auto scores = [&](auto S) {  // S^T = K Q^T
 #pragma unroll
-        for (int kb = 0; kb < KS; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
             sv[kb] = f32x16{};
 #pragma unroll
             for (int st = 0; st < L::STEPS; ++st)
-                sv[kb] = L::qk(*reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * (B0.value + kb) * ROWB]), q[st], sv[kb]);
+                sv[kb] = L::qk(*reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * kb * ROWB]), q[st], sv[kb]);
         }
     };
-    auto hide = [&](auto S, auto B0) {  // scores of what the query does not attend to: -infinity
+    auto hide = [&](auto S) {  // scores of what the query does not attend to: -infinity
 #pragma unroll
-        for (int kb = 0; kb < KS; ++kb) {
-            const int blk = wk * KB + B0.value + kb, jb = jpos[S.value] + 32 * blk;
+        for (int kb = 0; kb < KB; ++kb) {
+            const int blk = wk * KB + kb, jb = jpos[S.value] + 32 * blk;
             const uint32_t bits = static_cast<uint32_t>((blk < 2 ? valid[S.value][0] : valid[S.value][PIDS - 1]) >> (32 * (blk & 1)));
             // the block's keys that the query attends to, from the lane's first on
             const uint32_t see = (bits & below(p_hi - jb) & (~below(p_lo - jb) | below(a.sinks - jb))) >> (4 * hf);
@@ -337,7 +341,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     auto raise = [&]() {
         float mx = sv[0][0];
 #pragma unroll
-        for (int kb = 0; kb < KS; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 mx = fmaxf(mx, sv[kb][r]);
@@ -354,8 +358,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     };
     // weights, and O^T += V^T P^T one part of 16 keys behind them, so that a wavefront's products
     // and exponentials overlap
-    auto weigh = [&](auto S, auto B0) {
-        constexpr int PARTS = 2 * KS;
+    auto weigh = [&](auto S) {
+        constexpr int PARTS = 2 * KB;
         const float ref = m == -__builtin_inff() ? 0.f : m;
         float wt[PARTS][8];
         bf16x8 wb[PARTS];
@@ -370,7 +374,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
                     wb[x] = to_bf16x8(wt[x]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{wb[x][2 * e], wb[x][2 * e + 1]}, kOnes, l, false);
+                        l = add_pair(wb[x], e, l);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -378,7 +382,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
                 }
             }
             if (x > 0) {
-                const int row = 32 * (B0.value + (x - 1) / 2) + 16 * ((x - 1) % 2);
+                const int row = 16 * (x - 1);
                 if constexpr (EL == 2) {
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
@@ -443,19 +447,11 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         if (t + 1 < t1)
             start(Int<1 - S.value>{});
         if (seen(S)) {
-            const bool wh = whole(S);
-            scores(S, Int<0>{});
-            if (!wh)
-                hide(S, Int<0>{});
+            scores(S);
+            if (!whole(S))
+                hide(S);
             raise();
-            weigh(S, Int<0>{});
-            if constexpr (KB > KS) {
-                scores(S, Int<KS>{});
-                if (!wh)
-                    hide(S, Int<KS>{});
-                raise();
-                weigh(S, Int<KS>{});
-            }
+            weigh(S);
         }
     };
     if (t0 < t1)
@@ -625,19 +621,27 @@ void join(const AttnArgs &a, int nsplit, const float *part, const float2 *ml, hi
     k_attn_join<T, D, GROUPS><<<dim3(static_cast<unsigned>((R + RPW - 1) / RPW), a.KV, a.batch), 256, 0, st>>>(a, nsplit, part, ml);
 }
 
-// f(WM, WK, TK, WPE): the kernel shape for R rows per (stream, KV head).
+// f(WM, WK, TK, WPE): the kernel shape for R rows per (stream, KV head): row blocks of 32 and key
+// parts of a workgroup, keys of a tile, wavefronts per SIMD.
+//  bf16   up to 64 rows: 2 x 2 (16 rows a head group, 8 streams of 32,768, headdim 128: 107 us,
+//         115 us as 8 x 1); more: 8 x 1 (128 rows, headdim 64: 62 us, 77 us as 2 x 2)
+//  f32    up to 32 rows of headdim 64: 1 x 4 (32 rows, 8 streams of 4,096: 28 us, 32 us as 2 x 2,
+//         47 us as 4 x 1); up to 64 rows: 2 x 2 (64 rows: 34 us, 49 us as 4 x 1; headdim 128:
+//         58 us, 83 us); more: 4 x 1, whose products leave no room for more wavefronts
 template <typename T, int D, typename F>
 auto by_rows(int64_t R, F f)
 {
     if constexpr (sizeof(T) == 2) {
-        if (R <= 32)
-            return f.template operator()<T, D, 1, 4, 128, (D == 64 ? 2 : 1)>();
         if (R <= 64)
             return f.template operator()<T, D, 2, 2, 64, (D == 64 ? 3 : 2)>();
         return f.template operator()<T, D, 8, 1, 64, (D == 64 ? 4 : 2)>();
     } else {
-        if (R <= 32)
-            return f.template operator()<T, D, 1, (D == 64 ? 4 : 2), (D == 64 ? 128 : 64), 1>();
+        if constexpr (D == 64) {
+            if (R <= 32)
+                return f.template operator()<T, D, 1, 4, 128, 1>();
+        }
+        if (R <= 64)
+            return f.template operator()<T, D, 2, 2, 64, (D == 64 ? 2 : 1)>();
         return f.template operator()<T, D, 4, 1, (D == 64 ? 64 : 32), 2>();
     }
 }
