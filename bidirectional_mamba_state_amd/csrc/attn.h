@@ -73,17 +73,20 @@ __device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b)
     return s;
 }
 
+constexpr int64_t kMaxGroups = (int64_t{1} << 32) / 512 - 1;  // a grid's threads have to fit 32 bits
+
 // Launch plan of a step. A unit is one (stream, KV head, range of its keys); its row tiles read
 // the same keys, so they go to one XCD (its L2 then fetches them once), side by side in time.
 // Few units with many row tiles are cut into `sub` parts of every sub-th tile, so that all eight
 // XCDs have work. Workgroup id: XCD id % 8, and inside an XCD row tiles run fastest (rt_fast) or
 // slowest.
 struct AttnPlan {
-    int nrt, nsplit;                  // row tiles per (stream, KV head); ranges of its keys
-    int sub, nrt_sub, units, per_xcd; // parts per unit, row tiles per part, parts, parts per XCD
+    int nrt, nsplit;                   // row tiles per (stream, KV head); ranges of its keys
+    int sub, nrt_sub, units, per_xcd;  // parts per unit, row tiles per part, parts, parts per XCD
     int rt_fast;
     Divisor by_inner, by_units, by_kv, by_split;  // nrt_sub or per_xcd, units / sub, KV, nsplit
-    size_t ml_bytes, ws_bytes;        // workspace: maxima and sums first, then rows (0 unless split)
+    int64_t groups;                    // workgroups; more than kMaxGroups cannot be launched
+    size_t ml_bytes, ws_bytes;         // workspace: maxima and sums first, then rows (0 unless split)
 };
 
 AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);

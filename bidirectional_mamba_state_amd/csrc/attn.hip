@@ -154,7 +154,8 @@ extern "C" size_t bdssm_attn_step_workspace(const bdssm_attn_dims *dims, int32_t
     a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
     if (!rows_fit(a))
         return SIZE_MAX;
-    return attn_plan(a, dims->headdim, dims->dtype == BDSSM_BF16).ws_bytes;
+    const AttnPlan p = attn_plan(a, dims->headdim, dims->dtype == BDSSM_BF16);
+    return p.groups > kMaxGroups ? SIZE_MAX : p.ws_bytes;
 }
 
 extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,
@@ -186,6 +187,8 @@ extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm
         return BDSSM_ERR_UNSUPPORTED;
     const bool bf16 = dims->dtype == BDSSM_BF16;
     const AttnPlan p = attn_plan(a, dims->headdim, bf16);
+    if (p.groups > kMaxGroups)
+        return BDSSM_ERR_UNSUPPORTED;
     if (p.ws_bytes > 0) {
         if (!workspace || workspace_bytes < p.ws_bytes)
             return BDSSM_ERR_WORKSPACE;

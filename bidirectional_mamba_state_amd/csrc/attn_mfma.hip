@@ -655,40 +655,49 @@ struct PlanOf {
         AttnPlan p{};
         const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
         p.nrt = static_cast<int>((R + C::RT - 1) / C::RT);
-        // Ranges: the number that makes the workgroups take the fewest tiles in all, one after
-        // the other on a place of the GPU. A workgroup costs some tiles beside its own (its
-        // start and first copies, and where the keys are split its partial rows). Rows in order
-        // of their blocks come longest first and end together; without an order the rounds are
-        // whole and, streams being of unequal lengths, the last one ends half a workgroup late.
-        // float32 products fill a CU's matrix cores with one workgroup, so two that share one
-        // take turns; with bf16 all that fit run together. Measured at 64 streams of 16-32K
-        // tokens, 768 rows: 1495 us whole, 1250 in four ranges; at 8,192 ordered rows of 5 heads:
-        // 1020 us whole, 1077 in two.
+        const int64_t units = static_cast<int64_t>(a.batch) * a.KV;
+        auto deal = [&](int64_t ns) {  // the parts of a launch with ns ranges
+            const int64_t all = units * ns;
+            p.nsplit = static_cast<int>(ns);
+            p.sub = static_cast<int>(all >= 64 ? 1 : std::min<int64_t>(p.nrt, (64 + all - 1) / all));
+            p.nrt_sub = (p.nrt + p.sub - 1) / p.sub;
+            p.units = static_cast<int>(all * p.sub);
+            p.per_xcd = (p.units + 7) / 8;
+        };
+        // Ranges: the number with which an XCD's workgroups take the fewest tiles one after the
+        // other. A workgroup costs tiles beside its own: its start and first copies, and where
+        // the keys are split its partial rows and their join. The rounds are whole, and streams
+        // being of unequal lengths the last one ends half a workgroup late; only rows of a
+        // prompt in order, whose ranges grow with them, come longest first and end together.
+        // float32 products fill a CU's matrix cores with one workgroup, so that two take turns;
+        // with bf16 all that fit run together. Against the best of 1 to 24 ranges, the choice
+        // cost 3 % in the mean over 18 shapes and 20 % at most (64 streams of 16-32K tokens, 768
+        // rows: 1495 us whole, 1254 in the four that it takes; 564 float32 rows on 33,169
+        // tokens: 370 us in 17, 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two).
         const bool f32 = sizeof(T) == 4;
         const int64_t span = std::min<int64_t>(a.block_len, (C::RT + a.H / a.KV - 1) / (a.H / a.KV));
         int64_t keys = static_cast<int64_t>(a.max_len) + a.block_len;  // of one row tile, at most
         if (a.window)
             keys = std::min(keys, static_cast<int64_t>(a.window) + a.sinks + span + TK);
-        const int64_t tiles = (keys + TK - 1) / TK, units = static_cast<int64_t>(a.batch) * a.KV;
-        const int64_t slots = static_cast<int64_t>(device_cus()) * (f32 ? 1 : 4 * WPE / C::NW);
+        const int64_t tiles = (keys + TK - 1) / TK, slots = std::max(1, device_cus() / 8) * (f32 ? 1 : 4 * WPE / C::NW);
+        const int64_t start = f32 ? 2 : 3, split = f32 ? 1 : C::RT / 32;
+        const bool graded = a.block && 2 * static_cast<int64_t>(a.block_len) > a.max_len;
         int64_t ns = 1, best = INT64_MAX;
-        for (int64_t x = 1; x <= 64 && x <= (tiles + 3) / 4; ++x) {
-            const int64_t per = (tiles + x - 1) / x, all = units * p.nrt * x, each = per + 6 + (x > 1 ? 2 * C::RT / TK : 0);
-            const int64_t cost = a.block && all > slots ? 2 * all * each / slots : 2 * ((all + slots - 1) / slots) * each + per;
+        for (int64_t x = 1; x == 1 || (x <= 64 && x <= (tiles + 3) / 4 && units * p.nrt * x <= kMaxGroups / 8); ++x) {
+            deal(x);
+            const int64_t per = (tiles + x - 1) / x, each = per + start + (x > 1 ? split : 0);
+            const int64_t here = static_cast<int64_t>(p.per_xcd) * p.nrt_sub;  // workgroups of an XCD
+            const int64_t cost = graded && here > slots ? 2 * here * each / slots : 2 * ((here + slots - 1) / slots) * each + per;
             if (cost < best)
                 best = cost, ns = x;
         }
-        p.nsplit = static_cast<int>(ns);
-        const int64_t all = units * ns;
-        p.sub = static_cast<int>(all >= 64 ? 1 : std::min<int64_t>(p.nrt, (64 + all - 1) / all));
-        p.nrt_sub = (p.nrt + p.sub - 1) / p.sub;
-        p.units = static_cast<int>(all * p.sub);
-        p.per_xcd = (p.units + 7) / 8;
+        deal(ns);
         p.rt_fast = p.nrt_sub <= 4;
         p.by_inner = Divisor(p.rt_fast ? p.nrt_sub : p.per_xcd);
-        p.by_units = Divisor(all);
+        p.by_units = Divisor(units * ns);
         p.by_kv = Divisor(a.KV);
         p.by_split = Divisor(ns);
+        p.groups = 8ll * p.per_xcd * p.nrt_sub;
         const int64_t rows = static_cast<int64_t>(a.batch) * a.KV * ns * R;
         p.ml_bytes = ns > 1 ? static_cast<size_t>((rows * 8 + 255) / 256 * 256) : 0;
         p.ws_bytes = ns > 1 ? p.ml_bytes + static_cast<size_t>(rows) * D * 4 : 0;
@@ -708,7 +717,7 @@ struct Launch {
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
         k_attn<T, D, WM, WK, TK, WPE>
-            <<<dim3(static_cast<unsigned>(8 * p.per_xcd) * p.nrt_sub), C::THREADS, 0, st>>>(a, p, part, ml);
+            <<<dim3(static_cast<unsigned>(p.groups)), C::THREADS, 0, st>>>(a, p, part, ml);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.nsplit == 1)
             return e;
