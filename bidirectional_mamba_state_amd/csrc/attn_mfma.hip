@@ -28,7 +28,25 @@
 // Masks. Per tile a 64-bit mask says which keys exist, are held and are attended to by any row
 // of the workgroup; the values of the others (which may hold anything, NaN included) are cleared
 // in LDS before use. Scores are selected per element in tiles that some row of a wavefront does
-// not see whole; the other tiles skip that.
+// not see whole; the other tiles skip that. Values of keys that only some rows attend to may hold
+// infinities and NaN too: see repair.
+//
+// What bounds it, measured (a large bf16 matrix product reaches 1,258 TFLOP/s here, float32 153, a
+// large copy 4.9 TB/s both ways):
+//  - single tokens: HBM reads, 5.7 TB/s (64 streams x 32,768 tokens, 6 heads a group: 370 us);
+//  - a block of 32 on 262,144 tokens, 5 heads a group of 64: HBM and the vector unit together,
+//    3.7 TB/s at 590 TFLOP/s (146 us with its join of 8 us);
+//  - many rows, headdim 128: the matrix cores (42 % busy) share the clock with the exponentials
+//    (34 %) and with LDS, whose operand reads take half as long as the products; 970 TFLOP/s
+//    (a prompt chunk of 8,192 on 8,192, 20 heads: 1.06 ms);
+//  - many rows, headdim 64: the vector unit (54 % busy, matrix cores 37 %), half of whose work is
+//    the exponentials; 880 TFLOP/s on equal streams, 740 on unequal ones (64 x 16-32K tokens,
+//    768 rows: 1.23 ms), where short row tiles leave wavefronts idle;
+//  - float32: the matrix cores, 100 to 125 TFLOP/s.
+// Eight wavefronts of 32 rows, four a SIMD at headdim 64, did better than four of 64 (half the
+// LDS reads, but nothing hides a wavefront's own exponentials: 1340 against 1020 us on the
+// prompt), than a third stage, 128-key tiles or a scheduled overlap inside a wavefront (no
+// difference, or registers spilled).
 #include <algorithm>
 
 #include "attn.h"
@@ -104,6 +122,128 @@ struct Int {
     static constexpr int value = N;
 };
 
+// whether any lane of a workgroup of NW wavefronts found something
+template <int NW>
+__device__ __forceinline__ bool anyone(int *found, bool mine)
+{
+    const int any_mine = __ballot(mine) != 0;
+    if ((threadIdx.x & 63) == 0)
+        found[threadIdx.x >> 6] = any_mine;
+    __syncthreads();
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+        any |= found[i];
+    return __builtin_amdgcn_readfirstlane(any) != 0;
+}
+
+// A workgroup's rows and tiles of keys, as k_attn has them.
+struct RowRange {
+    int b, kvh, split, nsplit, r_first, r_end, t0, t1, ns, nw, w0, c0, tk, nwaves;
+};
+
+// An infinity or a NaN among the values of a key that some rows of a workgroup attend to reaches
+// its other rows through the matrix product, 0 x infinity being NaN. Where a workgroup's sums came
+// out so and such a key holds such a value, its rows are computed again here, one by one and without
+// the matrix cores, each from the keys that it attends to and no others. Returns whether it was so.
+// (Looking through the values of tiles that rows see in part, before use, cost 2 to 6 % of every
+// call; this costs nothing measurable until it is needed.)
+template <typename T, int D>
+__device__ __forceinline__ bool repair(const AttnArgs &a, const RowRange &in_lds, int *found, float *part, float2 *part_ml)
+{
+    const RowRange x = in_lds;
+    constexpr int EL = sizeof(T), ROWB = D * EL, PPR = ROWB / 16, PL = D / 64;  // PL: channels of a lane
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, G = static_cast<int>(a.by_group.d);
+    const AttnStream s = attn_stream(a, x.b);
+    const int end = s.len + (a.k ? s.n : 0), page = 1 << a.page_shift;
+    auto hi_of = [&](int p) {
+        if (a.block == 0)
+            return end;
+        const int64_t h = static_cast<int64_t>(a.by_block(p) + 1) * a.block;
+        return h < end ? static_cast<int>(h) : end;
+    };
+    auto lo_of = [&](int p) { return a.window == 0 || p < a.window ? 0 : p - a.window + 1; };
+    auto row_of = [&](int j, const void *pool, const void *own, int64_t stride) -> const T * {  // NULL: no such key
+        if (j >= s.len)
+            return j < end ? static_cast<const T *>(own) + (s.row0 + j - s.len) * stride + static_cast<int64_t>(x.kvh) * D : nullptr;
+        const int id = a.table[static_cast<int64_t>(x.b) * a.max_pages + (j >> a.page_shift)];
+        return id >= 0 && id < a.num_pages
+                   ? static_cast<const T *>(pool) + ((static_cast<int64_t>(id) * a.KV + x.kvh) * page + (j & (page - 1))) * D
+                   : nullptr;
+    };
+    float sum = 0.f;
+    auto look = [&](int from, int to) {  // a piece of a value row per lane and turn
+        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(to - from) * PPR; i += 64 * x.nwaves)
+            if (const T *v = row_of(from + static_cast<int>(i / PPR), a.vp, a.v, a.v_stride))
+                for (int e = 0; e < 16 / EL; ++e)
+                    sum = fmaf(static_cast<float>(v[i % PPR * (16 / EL) + e]), 0.f, sum);
+    };
+    const int pmin = s.len + a.by_group(x.r_first), pmax = s.len + a.by_group(x.r_end - 1);
+    look(lo_of(pmin), lo_of(pmax));
+    look(hi_of(pmin), hi_of(pmax));
+    const int mine = __ballot(sum != sum) != 0;
+    if (lane == 0)
+        found[w] = mine;
+    __syncthreads();
+    int any = 0;
+    for (int i = 0; i < x.nwaves; ++i)
+        any |= found[i];
+    if (!__builtin_amdgcn_readfirstlane(any))
+        return false;
+    const float sc = a.scale * kLog2e;
+    for (int row = x.r_first + w; row < x.r_end; row += x.nwaves) {
+        const int tok = a.by_group(row), head = x.kvh * G + row - tok * G, p = s.len + tok, hi = hi_of(p), lo = lo_of(p);
+        const T *q = static_cast<const T *>(a.q) + (s.row0 + tok) * a.q_stride + static_cast<int64_t>(head) * D;
+        float m = -__builtin_inff(), l = 0.f, o[PL] = {};
+        for (int t = x.t0; t < x.t1; ++t) {
+            const bool cached = t < x.ns + x.nw;
+            const int first = t < x.ns ? t * x.tk : cached ? (x.w0 + t - x.ns) * x.tk : s.len + (x.c0 + t - x.ns - x.nw) * x.tk;
+            const int stop = cached ? s.len : end;
+            for (int kk = 0; kk < x.tk; kk += 64) {
+                const int j = first + kk + lane;
+                const T *k = nullptr;
+                if (kk + lane < x.tk && j < stop && j < hi && (j >= lo || j < a.sinks))
+                    k = row_of(j, a.kp, a.k, a.k_stride);
+                float sj = 0.f;
+                if (k)
+                    for (int c = 0; c < D; ++c)
+                        sj = fmaf(static_cast<float>(q[c]), static_cast<float>(k[c]), sj);
+                float mx = k ? sj * sc : -__builtin_inff();
+                for (int y = 1; y < 64; y *= 2)
+                    mx = fmaxf(mx, __shfl_xor(mx, y));
+                mx = fmaxf(mx, m);
+                const float f = m == mx ? 1.f : __builtin_amdgcn_exp2f(m - mx);
+                const float wt = k ? __builtin_amdgcn_exp2f(fmaf(sj, sc, mx == -__builtin_inff() ? 0.f : -mx)) : 0.f;
+                float all = wt;
+                for (int y = 1; y < 64; y *= 2)
+                    all += __shfl_xor(all, y);
+                m = mx;
+                l = fmaf(l, f, all);
+                for (int c = 0; c < PL; ++c)
+                    o[c] *= f;
+                for (uint64_t left = __ballot(k != nullptr); left; left &= left - 1) {
+                    const int y = __builtin_ctzll(left);
+                    const T *v = row_of(first + kk + y, a.vp, a.v, a.v_stride) + lane * PL;
+                    const float wy = __shfl(wt, y);
+                    for (int c = 0; c < PL; ++c)
+                        o[c] = fmaf(wy, static_cast<float>(v[c]), o[c]);
+                }
+            }
+        }
+        if (x.nsplit == 1) {
+            T *out = static_cast<T *>(a.out) + ((s.row0 + tok) * a.H + head) * D + lane * PL;
+            for (int c = 0; c < PL; ++c)
+                out[c] = static_cast<T>(o[c] * (l > 0.f ? 1.f / l : l));
+        } else {
+            const int64_t to = ((static_cast<int64_t>(x.b) * a.KV + x.kvh) * x.nsplit + x.split) * a.block_len * G + row;
+            if (lane == 0)
+                part_ml[to] = make_float2(m, l);
+            for (int c = 0; c < PL; ++c)
+                part[to * D + lane * PL + c] = o[c];
+        }
+    }
+    return true;
+}
 template <typename T, int D, int WM, int WK, int TK>
 struct AttnCfg {
     static constexpr int NW = WM * WK, THREADS = 64 * NW, RT = 32 * WM;
@@ -120,7 +260,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     constexpr int NW = C::NW, ROWB = L::ROWB, PPR = ROWB / 16;
     constexpr int RPC = 1024 / ROWB;                // rows of a copy
     constexpr int NC = C::TILE_BYTES / 1024 / NW;   // copies of a wavefront per tile, of K and of V
-    constexpr int PIDS = (TK + 63) / 64;            // page number registers of a tile
+    constexpr int PIDS = (TK + 63) / 64;            // 64-key words of a tile's key mask
     constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile
     constexpr int EL = sizeof(T);
     constexpr uint64_t kAll = TK < 64 ? 0xffffffffull : ~0ull;  // a mask of keys with all of them
@@ -129,6 +269,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     // one array per stage and operand, so that reads of one need not wait for copies into another
     __shared__ __attribute__((aligned(16))) char k0[C::TILE_BYTES], v0[C::TILE_BYTES], k1[C::TILE_BYTES], v1[C::TILE_BYTES];
     __shared__ float2 ml[WK > 1 ? NW * 32 : 1];
+    __shared__ int odd[2][NW];  // what a wavefront found, and this workgroup's part: see repair
+    __shared__ RowRange mine;
     auto KBUF = [&](auto S) -> char * { return S.value == 0 ? k0 : k1; };
     auto VBUF = [&](auto S) -> char * { return S.value == 0 ? v0 : v1; };
 
@@ -165,7 +307,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         return h < end ? static_cast<int>(h) : end;
     };
     auto lo_of = [&](int p) { return a.window == 0 || p < a.window ? 0 : p - a.window + 1; };
-    const int lo_min = lo_of(s.len + a.by_group(r_first)), hi_max = hi_of(s.len + a.by_group(r_end - 1));
+    const int pmin = s.len + a.by_group(r_first), pmax = s.len + a.by_group(r_end - 1);
+    const int lo_min = lo_of(pmin), lo_max = lo_of(pmax), hi_min = hi_of(pmin), hi_max = hi_of(pmax);
     const int wr0 = r_first + wm * 32;
     const bool active = wr0 < r_end;
     const int wr1 = wr0 + 31 < r_end ? wr0 + 31 : r_end - 1;
@@ -180,6 +323,9 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const int c0 = c_lo / TK, nc = n > 0 && c_hi > c_lo ? (c_hi + TK - 1) / TK - c0 : 0;
     const int nt = ns + nw + nc;
     const int per = pl.by_split(nt + nsplit - 1), t0 = split * per, t1 = t0 + per < nt ? t0 + per : nt;
+
+    if ((lo_min != lo_max || hi_min != hi_max) && threadIdx.x == 0)
+        mine = RowRange{b, kvh, split, nsplit, r_first, r_end, t0, t1, ns, nw, w0, c0, TK, NW};
 
     struct Cursor {
         int t, start;  // tile, and its first key: cached position or index into the chunk
@@ -462,6 +608,25 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             step(Int<1>{}, t + 1);
     }
     l = half_sum(l);
+
+    // ---- repair: an infinity or a NaN among the values of a key that some of the workgroup's rows
+    // attend to has reached its other rows too, 0 x infinity being NaN
+    if (lo_min != lo_max || hi_min != hi_max) {
+        float sum = 0.f;  // 0 x an infinity or a NaN is NaN
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sum = fmaf(o[d][r], 0.f, sum);
+        if (anyone<NW>(odd[0], sum != sum)) {
+            // what it needs comes from the kernel's argument memory and from LDS again, so that
+            // nothing is kept in registers for it through the loop
+            auto *args = (const AttnArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+            asm volatile("" : "+s"(args));
+            if (repair<T, D>(*args, mine, odd[1], part, part_ml))
+                return;
+        }
+    }
 
     // ---- wavefronts that shared the rows: join in LDS, in wavefront order
     if constexpr (WK > 1) {

