@@ -206,12 +206,19 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current = None  # torch's functions for the current stream of a device and the current device
+
+
 def _stream(stream):
+    global _current
     if stream is None:
-        import torch
+        if _current is None:
+            import torch
+            torch.cuda.current_device()  # initializes the device
+            _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         # torch.cuda.current_stream().cuda_stream without the Stream object, whose construction
         # takes longer than the rest of a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current[0](_current[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -420,9 +427,15 @@ class DecodeGraph:
 # ------------------------------------------------- norms and attention around the Mamba layers
 # A decode step makes these calls for microseconds of GPU work, so their checks are plain
 # comparisons of what a tensor already holds.
+_torch_dtypes = None  # float32, bfloat16
+
+
 def _torch_dtype(dtype):
-    import torch
-    return torch.bfloat16 if dtype == BF16 else torch.float32
+    global _torch_dtypes
+    if _torch_dtypes is None:
+        import torch
+        _torch_dtypes = torch.float32, torch.bfloat16
+    return _torch_dtypes[dtype == BF16]
 
 
 def _expect(t, what, dtype, shape):
@@ -492,20 +505,20 @@ def residual_norm(nd, x, o, pre_w, x_out, u, post_w=None, gate=None, gain=None, 
     if pre_w is not None:
         _expect(pre_w, "pre_w", _torch_dtype(F32), shape[1:])
     gp = ap = sp = None
-    step = 0
+    step = 0  # between streams
     if gate is not None or gain is not None or shift is not None:
         per = (-(-nd.rows // nd.rows_per_stream) if nd.rows_per_stream > 0 else 0, nd.width)
-        steps = set()
+        steps = []
         if gate is not None:
             gp, step = _rows(gate, "gate", dt, per)
-            steps.add(step)
+            steps.append(step)
         if gain is not None:
             ap, step = _rows(gain, "gain", dt, per)
-            steps.add(step)
+            steps.append(step)
         if shift is not None:
             sp, step = _rows(shift, "shift", dt, per)
-            steps.add(step)
-        if len(steps) > 1:
+            steps.append(step)
+        if min(steps) != max(steps):
             raise ValueError("gate, gain and shift must have one stride between streams")
     r = Residual(_ptr(x), _ptr(o), _ptr(post_w), _ptr(pre_w), gp, ap, sp, step, res_scale)
     _check(load().bdssm_residual_norm(ctypes.byref(nd), ctypes.byref(r), _ptr(x_out), _ptr(u), _stream(stream)))
