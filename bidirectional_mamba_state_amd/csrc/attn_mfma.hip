@@ -835,20 +835,23 @@ struct PlanOf {
         // being of unequal lengths the last one ends half a workgroup late; only rows of a
         // prompt in order, whose ranges grow with them, come longest first and end together.
         // float32 products fill a CU's matrix cores with one workgroup, so that two take turns;
-        // with bf16 all that fit run together. Against the best of 1 to 24 ranges, the choice
-        // cost 3 % in the mean over 18 shapes and 20 % at most (64 streams of 16-32K tokens, 768
-        // rows: 1495 us whole, 1254 in the four that it takes; 564 float32 rows on 33,169
-        // tokens: 370 us in 17, 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two).
+        // with bf16 all that fit run together (64 streams of 16-32K tokens, 768 rows: 1495 us
+        // whole, 1254 in the four that it takes; 564 float32 rows on 33,169 tokens: 370 us in 17,
+        // 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two).
+        // A range has two tiles at least, so that copies overlap products (192 rows on 532 keys:
+        // 13.5 us in ranges of four tiles, 11.7); a float32 tile takes longer than its start and
+        // may stand alone (32 x 6 rows on 1,032 keys: 26.7 us in ranges of four, 15.9). A second
+        // launch costs as much as eight bf16 tiles (24 rows on 259 keys: 8.4 us whole, 11.7 in two).
         const bool f32 = sizeof(T) == 4;
         const int64_t span = std::min<int64_t>(a.block_len, (C::RT + a.H / a.KV - 1) / (a.H / a.KV));
         int64_t keys = static_cast<int64_t>(a.max_len) + a.block_len;  // of one row tile, at most
         if (a.window)
             keys = std::min(keys, static_cast<int64_t>(a.window) + a.sinks + span + TK);
         const int64_t tiles = (keys + TK - 1) / TK, slots = std::max(1, device_cus() / 8) * (f32 ? 1 : 4 * WPE / C::NW);
-        const int64_t start = f32 ? 2 : 3, split = f32 ? 1 : C::RT / 32;
+        const int64_t start = f32 ? 2 : 3, split = f32 ? 1 : 8;
         const bool graded = a.block && 2 * static_cast<int64_t>(a.block_len) > a.max_len;
         int64_t ns = 1, best = INT64_MAX;
-        for (int64_t x = 1; x == 1 || (x <= 64 && x <= (tiles + 3) / 4 && units * p.nrt * x <= kMaxGroups / 8); ++x) {
+        for (int64_t x = 1; x == 1 || (x <= 64 && x <= (f32 ? tiles : (tiles + 1) / 2) && units * p.nrt * x <= kMaxGroups / 8); ++x) {
             deal(x);
             const int64_t per = (tiles + x - 1) / x, each = per + start + (x > 1 ? split : 0);
             const int64_t here = static_cast<int64_t>(p.per_xcd) * p.nrt_sub;  // workgroups of an XCD
