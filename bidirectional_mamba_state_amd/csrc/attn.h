@@ -90,6 +90,10 @@ struct AttnPlan {
 };
 
 AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);
+// The most that the plan of any length up to a.max_len needs. The plan itself does not grow with
+// the length: a longer cache may fit whole rounds of workgroups with fewer ranges. SIZE_MAX: more
+// rows than a launch has threads for.
+size_t attn_workspace(const AttnArgs &a, int D, bool bf16);
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 
 }  // namespace bdssm

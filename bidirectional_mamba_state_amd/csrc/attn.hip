@@ -155,8 +155,7 @@ extern "C" size_t bdssm_attn_step_workspace(const bdssm_attn_dims *dims, int32_t
     a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
     if (!rows_fit(a))
         return SIZE_MAX;
-    const AttnPlan p = attn_plan(a, dims->headdim, dims->dtype == BDSSM_BF16);
-    return p.groups > kMaxGroups ? SIZE_MAX : p.ws_bytes;
+    return attn_workspace(a, dims->headdim, dims->dtype == BDSSM_BF16);
 }
 
 extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,

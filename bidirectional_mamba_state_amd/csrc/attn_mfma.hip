@@ -48,6 +48,7 @@
 // prompt), than a third stage, 128-key tiles or a scheduled overlap inside a wavefront (no
 // difference, or registers spilled).
 #include <algorithm>
+#include <cmath>
 
 #include "attn.h"
 #include "internal.h"
@@ -811,65 +812,152 @@ auto by_rows(int64_t R, F f)
     }
 }
 
-struct PlanOf {
+// Launch plan and workspace of one kernel shape.
+template <typename T, int D, int WM, int WK, int TK, int WPE>
+struct Planner {
+    using C = AttnCfg<T, D, WM, WK, TK>;
+    static constexpr bool f32 = sizeof(T) == 4;
+    // Ranges: the number with which an XCD's workgroups take the fewest tiles one after the
+    // other. A workgroup costs tiles beside its own: its start and first copies, and where
+    // the keys are split its partial rows and their join. The rounds are whole, and streams
+    // being of unequal lengths the last one ends half a workgroup late; only rows of a
+    // prompt in order, whose ranges grow with them, come longest first and end together.
+    // float32 products fill a CU's matrix cores with one workgroup, so that two take turns;
+    // with bf16 all that fit run together (64 streams of 16-32K tokens, 768 rows: 1495 us
+    // whole, 1254 in the four that it takes; 564 float32 rows on 33,169 tokens: 370 us in 17,
+    // 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two).
+    // A range has two tiles at least, so that copies overlap products (192 rows on 532 keys:
+    // 13.5 us in ranges of four tiles, 11.7); a float32 tile takes longer than its start and
+    // may stand alone (32 x 6 rows on 1,032 keys: 26.7 us in ranges of four, 15.9). A second
+    // launch costs as much as eight bf16 tiles (24 rows on 259 keys: 8.4 us whole, 11.7 in two).
+    static constexpr int64_t kStart = f32 ? 2 : 3, kSplit = f32 ? 1 : 8;
+    static constexpr int kMostRanges = 64;
     const AttnArgs &a;
-    template <typename T, int D, int WM, int WK, int TK, int WPE>
-    AttnPlan operator()() const
+    int64_t R, units, slots;  // rows per unit, (stream, KV head) pairs, workgroups of an XCD at a time
+    int nrt;
+    explicit Planner(const AttnArgs &args)
+        : a(args), R(static_cast<int64_t>(a.block_len) * (a.H / a.KV)), units(static_cast<int64_t>(a.batch) * a.KV),
+          slots(std::max(1, device_cus() / 8) * (f32 ? 1 : 4 * WPE / C::NW)), nrt(static_cast<int>((R + C::RT - 1) / C::RT))
     {
-        using C = AttnCfg<T, D, WM, WK, TK>;
-        AttnPlan p{};
-        const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
-        p.nrt = static_cast<int>((R + C::RT - 1) / C::RT);
-        const int64_t units = static_cast<int64_t>(a.batch) * a.KV;
-        auto deal = [&](int64_t ns) {  // the parts of a launch with ns ranges
-            const int64_t all = units * ns;
-            p.nsplit = static_cast<int>(ns);
-            p.sub = static_cast<int>(all >= 64 ? 1 : std::min<int64_t>(p.nrt, (64 + all - 1) / all));
-            p.nrt_sub = (p.nrt + p.sub - 1) / p.sub;
-            p.units = static_cast<int>(all * p.sub);
-            p.per_xcd = (p.units + 7) / 8;
-        };
-        // Ranges: the number with which an XCD's workgroups take the fewest tiles one after the
-        // other. A workgroup costs tiles beside its own: its start and first copies, and where
-        // the keys are split its partial rows and their join. The rounds are whole, and streams
-        // being of unequal lengths the last one ends half a workgroup late; only rows of a
-        // prompt in order, whose ranges grow with them, come longest first and end together.
-        // float32 products fill a CU's matrix cores with one workgroup, so that two take turns;
-        // with bf16 all that fit run together (64 streams of 16-32K tokens, 768 rows: 1495 us
-        // whole, 1254 in the four that it takes; 564 float32 rows on 33,169 tokens: 370 us in 17,
-        // 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two).
-        // A range has two tiles at least, so that copies overlap products (192 rows on 532 keys:
-        // 13.5 us in ranges of four tiles, 11.7); a float32 tile takes longer than its start and
-        // may stand alone (32 x 6 rows on 1,032 keys: 26.7 us in ranges of four, 15.9). A second
-        // launch costs as much as eight bf16 tiles (24 rows on 259 keys: 8.4 us whole, 11.7 in two).
-        const bool f32 = sizeof(T) == 4;
+    }
+    int64_t tiles(int64_t max_len) const  // of one row tile, at most
+    {
         const int64_t span = std::min<int64_t>(a.block_len, (C::RT + a.H / a.KV - 1) / (a.H / a.KV));
-        int64_t keys = static_cast<int64_t>(a.max_len) + a.block_len;  // of one row tile, at most
+        int64_t keys = max_len + a.block_len;
         if (a.window)
             keys = std::min(keys, static_cast<int64_t>(a.window) + a.sinks + span + TK);
-        const int64_t tiles = (keys + TK - 1) / TK, slots = std::max(1, device_cus() / 8) * (f32 ? 1 : 4 * WPE / C::NW);
-        const int64_t start = f32 ? 2 : 3, split = f32 ? 1 : 8;
-        const bool graded = a.block && 2 * static_cast<int64_t>(a.block_len) > a.max_len;
+        return (keys + TK - 1) / TK;
+    }
+    int64_t candidates(int64_t tiles) const  // 1 to so many ranges come into question
+    {
+        return std::max<int64_t>(1, std::min({static_cast<int64_t>(kMostRanges), f32 ? tiles : (tiles + 1) / 2,
+                                              kMaxGroups / 8 / (units * nrt)}));
+    }
+    AttnPlan deal(int64_t ns) const  // the parts of a launch with ns ranges
+    {
+        AttnPlan p{};
+        const int64_t all = units * ns;
+        p.nrt = nrt;
+        p.nsplit = static_cast<int>(ns);
+        p.sub = static_cast<int>(all >= 64 ? 1 : std::min<int64_t>(nrt, (64 + all - 1) / all));
+        p.nrt_sub = (nrt + p.sub - 1) / p.sub;
+        p.units = static_cast<int>(all * p.sub);
+        p.per_xcd = (p.units + 7) / 8;
+        return p;
+    }
+    int64_t per_xcd(int64_t ns) const  // workgroups of an XCD
+    {
+        const AttnPlan p = deal(ns);
+        return static_cast<int64_t>(p.per_xcd) * p.nrt_sub;
+    }
+    bool graded(int64_t max_len) const { return a.block && 2 * static_cast<int64_t>(a.block_len) > max_len; }
+    AttnPlan plan() const
+    {
+        const int64_t nt = tiles(a.max_len), top = candidates(nt);
+        const bool by_length = graded(a.max_len);
         int64_t ns = 1, best = INT64_MAX;
-        for (int64_t x = 1; x == 1 || (x <= 64 && x <= (f32 ? tiles : (tiles + 1) / 2) && units * p.nrt * x <= kMaxGroups / 8); ++x) {
-            deal(x);
-            const int64_t per = (tiles + x - 1) / x, each = per + start + (x > 1 ? split : 0);
-            const int64_t here = static_cast<int64_t>(p.per_xcd) * p.nrt_sub;  // workgroups of an XCD
-            const int64_t cost = graded && here > slots ? 2 * here * each / slots : 2 * ((here + slots - 1) / slots) * each + per;
+        for (int64_t x = 1; x <= top; ++x) {
+            const int64_t per = (nt + x - 1) / x, each = per + kStart + (x > 1 ? kSplit : 0), here = per_xcd(x);
+            const int64_t cost = by_length && here > slots ? 2 * here * each / slots : 2 * ((here + slots - 1) / slots) * each + per;
             if (cost < best)
                 best = cost, ns = x;
         }
-        deal(ns);
+        AttnPlan p = deal(ns);
         p.rt_fast = p.nrt_sub <= 4;
         p.by_inner = Divisor(p.rt_fast ? p.nrt_sub : p.per_xcd);
         p.by_units = Divisor(units * ns);
         p.by_kv = Divisor(a.KV);
         p.by_split = Divisor(ns);
         p.groups = 8ll * p.per_xcd * p.nrt_sub;
-        const int64_t rows = static_cast<int64_t>(a.batch) * a.KV * ns * R;
-        p.ml_bytes = ns > 1 ? static_cast<size_t>((rows * 8 + 255) / 256 * 256) : 0;
-        p.ws_bytes = ns > 1 ? p.ml_bytes + static_cast<size_t>(rows) * D * 4 : 0;
+        p.ml_bytes = ns > 1 ? ml_bytes(ns) : 0;
+        p.ws_bytes = ns > 1 ? bytes(ns) : 0;
         return p;
+    }
+    size_t ml_bytes(int64_t ns) const { return static_cast<size_t>((units * R * ns * 8 + 255) / 256 * 256); }
+    size_t bytes(int64_t ns) const { return ml_bytes(ns) + static_cast<size_t>(units * R * ns) * D * 4; }
+    // An upper bound of the ranges that plan() takes for any length whose tiles are lo to hi
+    // (`least` or more; exact for half of the shapes, a third above for one in ten). In tiles per
+    // range p = ceil(tiles / x), x ranges cost per p + fixed, and y < x ranges
+    // per' ceil(tiles / y) + fixed' <= per' (p x + y - 1) / y + fixed'. x is taken only if it
+    // costs less than every such y: each leaves an interval of p, and x is out where none is left.
+    int64_t most_ranges(bool by_length, int64_t lo, int64_t hi, int64_t least) const
+    {
+        struct {
+            double per, fixed;
+        } cost[kMostRanges + 1];
+        const int top = static_cast<int>(candidates(hi));
+        for (int x = 1; x <= top; ++x) {
+            const int64_t here = per_xcd(x);
+            const double turns = by_length && here > slots ? 2. * here / slots : 2. * ((here + slots - 1) / slots);
+            cost[x] = {by_length && here > slots ? turns : turns + 1, turns * (kStart + (x > 1 ? kSplit : 0))};
+        }
+        for (int x = top; x > least; --x) {
+            double from = std::max<double>((lo + x - 1) / x, f32 ? 1 : 2), to = (hi + x - 1) / x;
+            for (int y = x - 1; y > 0 && from <= to; --y) {
+                const double slope = cost[x].per - cost[y].per * x / y;
+                const double room = cost[y].fixed - cost[x].fixed + cost[y].per * (y - 1) / y;  // slope p < room
+                if (slope > 0)
+                    to = std::min(to, std::floor(room / slope + 1e-6));
+                else if (slope < 0)
+                    from = std::max(from, std::ceil(room / slope - 1e-6));
+                else if (room <= 0)
+                    to = 0;
+            }
+            if (from <= to)
+                return x;
+        }
+        return least;
+    }
+    // what any length up to max_len can need; SIZE_MAX: more rows than a launch has threads for
+    size_t workspace() const
+    {
+        if (8 * per_xcd(1) > kMaxGroups)
+            return SIZE_MAX;
+        const int64_t turn = a.block ? 2ll * a.block_len : 0;  // lengths below it are graded
+        int64_t most = 1;
+        if (a.max_len >= turn)
+            most = most_ranges(false, tiles(turn), tiles(a.max_len), most);
+        if (turn > 0)
+            most = most_ranges(true, tiles(0), tiles(std::min<int64_t>(a.max_len, turn - 1)), most);
+        return most > 1 ? bytes(most) : 0;
+    }
+};
+
+struct PlanOf {
+    const AttnArgs &a;
+    template <typename T, int D, int WM, int WK, int TK, int WPE>
+    AttnPlan operator()() const
+    {
+        return Planner<T, D, WM, WK, TK, WPE>(a).plan();
+    }
+};
+
+struct WorkspaceOf {
+    const AttnArgs &a;
+    template <typename T, int D, int WM, int WK, int TK, int WPE>
+    size_t operator()() const
+    {
+        return Planner<T, D, WM, WK, TK, WPE>(a).workspace();
     }
 };
 
@@ -910,6 +998,11 @@ auto by_type(int D, bool bf16, int64_t R, F f)
 AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16)
 {
     return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), PlanOf{a});
+}
+
+size_t attn_workspace(const AttnArgs &a, int D, bool bf16)
+{
+    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), WorkspaceOf{a});
 }
 
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st)

@@ -99,8 +99,7 @@ class AttentionLayer:
         q, k, v = (qkv[:, s * 64 : (s + h) * 64].view(n, h, 64) for s, h in ((0, H), (H, KV), (H + KV, KV)))
         mask = m.mask if mode == "denoise" else m.block_mask
         out = torch.empty((n, H, 64), dtype=u.dtype, device="cuda")
-        need = bdssm.attn_step_workspace(m.attn, tokens, self.cache.max_len, mask)
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+        ws = m.ws if tokens == BLOCK else m.workspace(tokens, self.cache.max_len, mask)
         bdssm.attn_step(m.attn, tokens, q, k, v, self.cache, mask, out, ws)
         if mode != "denoise":
             bdssm.kv_append(m.attn, tokens, k, v, self.cache, m.lens[1])
@@ -123,8 +122,13 @@ class HybridStack:
         self.block_mask = bdssm.attn_mask(0.125, BLOCK, window, sinks)  # clean tokens: by blocks
         self.layers = [AttentionLayer(self, g) if (i + 1) % (attn_every + 1) == 0 else MambaLayer(self, mamba_heads, g)
                        for i in range(layers)]
+        # a block's workspace: the longest cache's serves every length, the layers take turns
+        self.ws = max((self.workspace(BLOCK, per * self.page, m) for m in (self.mask, self.block_mask)), key=torch.numel)
         self.norm_w = torch.ones(width, device="cuda")
         self.w_time = self.weight(g, 64, 3 * width * layers)
+
+    def workspace(self, tokens, max_len, mask):
+        return torch.empty(bdssm.attn_step_workspace(self.attn, tokens, max_len, mask), dtype=torch.uint8, device="cuda")
 
     def weight(self, g, rows, cols):
         return (torch.randn((rows, cols), generator=g, device="cuda") / math.sqrt(rows)).bfloat16()

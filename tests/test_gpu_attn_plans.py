@@ -1,0 +1,29 @@
+"""Launch plans of bdssm_attn_step on the GPU: one workspace for many lengths."""
+import numpy as np
+import pytest
+
+from bidirectional_mamba_state_amd import bdssm
+from test_gpu_attn import Case, _case, _np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H,KV,lens", [(40, 8, (5600, 6016, 7296, 7777, 8064)), (24, 4, (7616, 8000, 8064))])
+def test_the_longest_caches_workspace_serves_shorter_ones(H, KV, lens):
+    """A block of 32 on 8,192 cached tokens takes fewer ranges than on some shorter caches."""
+    import torch
+    longest = 8192
+    c = Case([longest], [32], H=H, KV=KV, page=32)
+    ws = torch.full((bdssm.attn_step_workspace(c.ad, 32, longest, c.mask),), 255, dtype=torch.uint8, device="cuda")
+    for n in (*lens, 1000, 1, longest):
+        _case(f"{H} heads over {KV}, {n} of {longest} tokens")
+        c.lens, c.max_len = [n], n
+        c.lens_d.fill_(n)
+        c.cache.max_len = n
+        out = torch.full_like(c.q, float("nan"))
+        bdssm.attn_step(c.ad, 32, c.q, c.k, c.v, c.cache, c.mask, out, ws)
+        torch.cuda.synchronize()
+        if n in (lens[0], 1000):
+            want, tol = c.want()
+            assert np.all(np.abs(_np(out) - want) <= tol)
+        assert torch.equal(out, c.run())  # with a workspace of its own length
