@@ -47,6 +47,8 @@
 // LDS reads, but nothing hides a wavefront's own exponentials: 1340 against 1020 us on the
 // prompt), than a third stage, 128-key tiles or a scheduled overlap inside a wavefront (no
 // difference, or registers spilled).
+#include <limits.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -820,12 +822,13 @@ struct Planner {
     // Ranges: the number with which an XCD's workgroups take the fewest tiles one after the
     // other. A workgroup costs tiles beside its own: its start and first copies, and where
     // the keys are split its partial rows and their join. The rounds are whole, and streams
-    // being of unequal lengths the last one ends half a workgroup late; only rows of a
-    // prompt in order, whose ranges grow with them, come longest first and end together.
+    // being of unequal lengths the last one ends half a workgroup late; only row
+    // tiles that come longest first (`graded`) end together.
     // float32 products fill a CU's matrix cores with one workgroup, so that two take turns;
     // with bf16 all that fit run together (64 streams of 16-32K tokens, 768 rows: 1495 us
     // whole, 1254 in the four that it takes; 564 float32 rows on 33,169 tokens: 370 us in 17,
-    // 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two).
+    // 285 in 25; a prompt of 8,192: 1020 us whole, 1077 in two; 4,096 tokens of 20 heads of 128,
+    // window 512 without order: 142 us whole, 159 in two).
     // A range has two tiles at least, so that copies overlap products (192 rows on 532 keys:
     // 13.5 us in ranges of four tiles, 11.7); a float32 tile takes longer than its start and
     // may stand alone (32 x 6 rows on 1,032 keys: 26.7 us in ranges of four, 15.9). A second
@@ -840,12 +843,16 @@ struct Planner {
           slots(std::max(1, device_cus() / 8) * (f32 ? 1 : 4 * WPE / C::NW)), nrt(static_cast<int>((R + C::RT - 1) / C::RT))
     {
     }
-    int64_t tiles(int64_t max_len) const  // of one row tile, at most
+    // keys of one row tile, at most; a window only looks back, and ahead of a row tile are the
+    // rest of its last row's block, or the whole chunk (`ahead`)
+    int64_t span() const { return std::min<int64_t>(a.block_len, (C::RT + a.H / a.KV - 1) / (a.H / a.KV)); }
+    int64_t back() const { return static_cast<int64_t>(a.window) + a.sinks + span(); }
+    int64_t ahead() const { return std::min<int64_t>(a.block_len - span(), a.block ? a.block - 1 : INT_MAX); }
+    int64_t tiles(int64_t max_len) const
     {
-        const int64_t span = std::min<int64_t>(a.block_len, (C::RT + a.H / a.KV - 1) / (a.H / a.KV));
         int64_t keys = max_len + a.block_len;
         if (a.window)
-            keys = std::min(keys, static_cast<int64_t>(a.window) + a.sinks + span + TK);
+            keys = std::min(keys, back() + ahead() + TK);
         return (keys + TK - 1) / TK;
     }
     int64_t candidates(int64_t tiles) const  // 1 to so many ranges come into question
@@ -870,11 +877,25 @@ struct Planner {
         const AttnPlan p = deal(ns);
         return static_cast<int64_t>(p.per_xcd) * p.nrt_sub;
     }
-    bool graded(int64_t max_len) const { return a.block && 2 * static_cast<int64_t>(a.block_len) > max_len; }
+    // The lengths for which a unit's row tiles come longest first and end together: a prompt in
+    // order, and a window without order where most of a row tile's keys are ahead of it. With
+    // float32 the latter still gains from whole rounds (2 x 1,031 tokens of 16 heads, window 512:
+    // 152 us whole, 103 in two).
+    struct Lengths {
+        int64_t from, to;  // [from, to)
+    };
+    Lengths graded() const
+    {
+        if (a.block)
+            return {0, 2ll * a.block_len};
+        if (!f32 && a.window && 2 * back() < back() + ahead() + TK)
+            return {std::max<int64_t>(0, 2 * back() + 1 - a.block_len), INT64_MAX};
+        return {0, 0};
+    }
     AttnPlan plan() const
     {
         const int64_t nt = tiles(a.max_len), top = candidates(nt);
-        const bool by_length = graded(a.max_len);
+        const bool by_length = a.max_len >= graded().from && a.max_len < graded().to;
         int64_t ns = 1, best = INT64_MAX;
         for (int64_t x = 1; x <= top; ++x) {
             const int64_t per = (nt + x - 1) / x, each = per + kStart + (x > 1 ? kSplit : 0), here = per_xcd(x);
@@ -933,12 +954,16 @@ struct Planner {
     {
         if (8 * per_xcd(1) > kMaxGroups)
             return SIZE_MAX;
-        const int64_t turn = a.block ? 2ll * a.block_len : 0;  // lengths below it are graded
+        const Lengths g = graded();
         int64_t most = 1;
-        if (a.max_len >= turn)
-            most = most_ranges(false, tiles(turn), tiles(a.max_len), most);
-        if (turn > 0)
-            most = most_ranges(true, tiles(0), tiles(std::min<int64_t>(a.max_len, turn - 1)), most);
+        auto lengths = [&](bool by_length, int64_t from, int64_t to) {
+            to = std::min<int64_t>(to, a.max_len + 1ll);
+            if (from < to)
+                most = most_ranges(by_length, tiles(from), tiles(to - 1), most);
+        };
+        lengths(false, 0, g.from);
+        lengths(true, g.from, g.to);
+        lengths(false, std::max(g.from, g.to), INT64_MAX);
         return most > 1 ? bytes(most) : 0;
     }
 };

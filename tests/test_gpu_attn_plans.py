@@ -27,3 +27,13 @@ def test_the_longest_caches_workspace_serves_shorter_ones(H, KV, lens):
             want, tol = c.want()
             assert np.all(np.abs(_np(out) - want) <= tol)
         assert torch.equal(out, c.run())  # with a workspace of its own length
+
+
+@pytest.mark.parametrize("dtype", [bdssm.BF16, bdssm.F32])
+@pytest.mark.parametrize("block", [0, 250])
+def test_window_over_a_chunk_that_looks_ahead(dtype, block):
+    """Queries that see few keys back and many ahead, their keys split over workgroups."""
+    _case(f"window without order, {dtype} {block}")
+    c = Case([90], [700], H=2, KV=1, dtype=dtype, block=block, window=37, sinks=5, page=32)
+    assert bdssm.attn_step_workspace(c.ad, 700, 90, c.mask) > 0
+    c.check("window without order")
