@@ -150,7 +150,8 @@ struct RowRange {
 // out so and such a key holds such a value, its rows are computed again here, one by one and without
 // the matrix cores, each from the keys that it attends to and no others. Returns whether it was so.
 // (Looking through the values of tiles that rows see in part, before use, cost 2 to 6 % of every
-// call; this costs nothing measurable until it is needed.)
+// call; this costs nothing measurable until it is needed, and much then: a NaN among the last
+// values of a prompt of 8,192 tokens on 8,192, 1.1 ms to 196 ms, which is one workgroup's 256 rows.)
 template <typename T, int D>
 __device__ __forceinline__ bool repair(const AttnArgs &a, const RowRange &in_lds, int *found, float *part, float2 *part_ml)
 {
@@ -204,9 +205,11 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const RowRange &in_lds
             const int stop = cached ? s.len : end;
             for (int kk = 0; kk < x.tk; kk += 64) {
                 const int j = first + kk + lane;
-                const T *k = nullptr;
-                if (kk + lane < x.tk && j < stop && j < hi && (j >= lo || j < a.sinks))
+                const T *k = nullptr, *v = nullptr;
+                if (kk + lane < x.tk && j < stop && j < hi && (j >= lo || j < a.sinks)) {
                     k = row_of(j, a.kp, a.k, a.k_stride);
+                    v = row_of(j, a.vp, a.v, a.v_stride);
+                }
                 float sj = 0.f;
                 if (k)
                     for (int c = 0; c < D; ++c)
@@ -216,7 +219,10 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const RowRange &in_lds
                     mx = fmaxf(mx, __shfl_xor(mx, y));
                 mx = fmaxf(mx, m);
                 const float f = m == mx ? 1.f : __builtin_amdgcn_exp2f(m - mx);
-                const float wt = k ? __builtin_amdgcn_exp2f(fmaf(sj, sc, mx == -__builtin_inff() ? 0.f : -mx)) : 0.f;
+                // rounded like the weights of the matrix product, before their sum is taken
+                const float wt =
+                    k ? static_cast<float>(static_cast<T>(__builtin_amdgcn_exp2f(fmaf(sj, sc, mx == -__builtin_inff() ? 0.f : -mx))))
+                      : 0.f;
                 float all = wt;
                 for (int y = 1; y < 64; y *= 2)
                     all += __shfl_xor(all, y);
@@ -226,10 +232,10 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const RowRange &in_lds
                     o[c] *= f;
                 for (uint64_t left = __ballot(k != nullptr); left; left &= left - 1) {
                     const int y = __builtin_ctzll(left);
-                    const T *v = row_of(first + kk + y, a.vp, a.v, a.v_stride) + lane * PL;
+                    const T *vy = reinterpret_cast<const T *>(__shfl(reinterpret_cast<uintptr_t>(v), y)) + lane * PL;
                     const float wy = __shfl(wt, y);
                     for (int c = 0; c < PL; ++c)
-                        o[c] = fmaf(wy, static_cast<float>(v[c]), o[c]);
+                        o[c] = fmaf(wy, static_cast<float>(vy[c]), o[c]);
                 }
             }
         }

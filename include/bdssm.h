@@ -529,7 +529,8 @@ bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const bdssm_residu
  * its maximum, sum and the weighted sum of values in float32; with bf16 values each weight is
  * rounded to bf16 for the matrix product. A query that attends to nothing gets zeros. What keys
  * and values hold that a query does not attend to never reaches its row, infinities and NaN
- * included.
+ * included; but beside a row that does attend to one, sums may be taken in another order and
+ * weights rounded from another reference, so a row's last bits may depend on it.
  */
 typedef struct {
     int32_t batch;     /* streams */
