@@ -16,9 +16,12 @@
 // by reading V in that order.
 //
 // Softmax. Scores are scaled to powers of two (scale log2 e folded into one fma before exp2).
-// The reference m of a query is raised, and its sums rescaled, only when a tile's maximum
-// exceeds it by more than 8: weights then stay below 2^8, which float32 sums and bf16 weights
-// hold as well as weights below 1.
+// The reference m of a query is set 8 above the maximum, and raised, with its sums rescaled, only
+// when a tile's maximum exceeds it: weights are 1 at most (a sum overflows only where the values'
+// own would), and the largest is 2^-8 at least, which float32 sums and bf16 weights hold as well.
+// With bf16 values each weight is rounded to bf16: the matrix cores take both factors in one type,
+// and float32 products run at an eighth of the rate. Their sum is of the rounded weights, so that
+// the weights that are used add up to one exactly; it is float32, as are maxima and weighted sums.
 //
 // Copies. Keys and values go from the pages (or the chunk's rows) straight into LDS, 1 KB a
 // copy, each copy inside one page (a page holds 16 tokens or more, a copy 8 at most); the
@@ -64,7 +67,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kRaise = 8.f;  // see "Softmax" above
+constexpr float kAbove = 8.f;  // see "Softmax" above
 
 template <typename T, int D>
 struct Tile;
@@ -217,7 +220,7 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const RowRange &in_lds
                 float mx = k ? sj * sc : -__builtin_inff();
                 for (int y = 1; y < 64; y *= 2)
                     mx = fmaxf(mx, __shfl_xor(mx, y));
-                mx = fmaxf(mx, m);
+                mx = mx > m ? mx + kAbove : m;  // the reference, as in k_attn
                 const float f = m == mx ? 1.f : __builtin_amdgcn_exp2f(m - mx);
                 // rounded like the weights of the matrix product, before their sum is taken
                 const float wt =
@@ -501,8 +504,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             for (int r = 0; r < 16; ++r)
                 mx = fmaxf(mx, sv[kb][r]);
         mx = half_max(mx) * sc;
-        if (__ballot(mx > m + kRaise)) {
-            const float mn = fmaxf(m, mx);
+        if (__ballot(mx > m)) {
+            const float mn = fmaxf(m, mx + kAbove);
             const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);  // equal infinities: 1
             m = mn;
             l *= f;

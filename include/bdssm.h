@@ -527,7 +527,9 @@ bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const bdssm_residu
  * and window = 0 or p - j < window or j < sinks (a sliding window that looks `window` tokens
  * back, its own among them, beside the first `sinks` tokens). The softmax is over scale * q.k,
  * its maximum, sum and the weighted sum of values in float32; with bf16 values each weight is
- * rounded to bf16 for the matrix product. A query that attends to nothing gets zeros. What keys
+ * rounded to bf16 for the matrix product. No weight exceeds 1 before the division by their sum,
+ * so that a result is finite where the sum of the values' magnitudes is. A query that attends to
+ * nothing gets zeros. What keys
  * and values hold that a query does not attend to never reaches its row, infinities and NaN
  * included; but beside a row that does attend to one, sums may be taken in another order and
  * weights rounded from another reference, so a row's last bits may depend on it.
