@@ -206,19 +206,26 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_current = None  # torch's functions for the current stream of a device and the current device
+def _current_stream():
+    """A function for the current stream's handle."""
+    import torch
+    torch.cuda.current_device()  # initializes the device
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    # the same without the Stream object, whose construction takes longer than the rest of a call
+    return lambda: raw(device())
+
+
+_current = None
 
 
 def _stream(stream):
     global _current
     if stream is None:
         if _current is None:
-            import torch
-            torch.cuda.current_device()  # initializes the device
-            _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        # torch.cuda.current_stream().cuda_stream without the Stream object, whose construction
-        # takes longer than the rest of a call
-        return _current[0](_current[1]())
+            _current = _current_stream()
+        return _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
