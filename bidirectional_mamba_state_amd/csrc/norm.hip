@@ -121,6 +121,14 @@ __device__ __forceinline__ void store8(T *p, int c, int n, const float (&f)[8])
 // z / (1 + exp(-z)); exp overflows to infinity below z = -88, where the result is -0
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
+// 1 / sqrt(v); the instruction takes numbers below 2^-126 for zero (a row of zeros with an eps
+// that small would be 0 x infinity)
+__device__ __forceinline__ float inv_sqrt(float v)
+{
+    const bool tiny = v < 0x1p-126f;
+    return __builtin_amdgcn_rsqf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p32f : 1.f);
+}
+
 // Sum over the LPR lanes of a row, in every one of them. `red`: four floats of LDS of this sum's
 // own (LPR = 256 only), so that one barrier is enough.
 template <int LPR>
@@ -168,7 +176,7 @@ __device__ __forceinline__ void normalize(float (&x)[VPT][8], int lane, int n, f
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             s = fmaf(x[i][k], x[i][k], s);
-    const float r = __builtin_amdgcn_rsqf(row_sum<LPR>(s, red + 4) * inv + eps);
+    const float r = inv_sqrt(row_sum<LPR>(s, red + 4) * inv + eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
