@@ -424,6 +424,12 @@ int64_t span(int64_t rows, int64_t stride, int64_t width, int e)
     return rows > 0 ? ((rows - 1) * stride + width) * e : 0;
 }
 
+// whether span() of these is a number of 64 bits
+bool span_fits(int64_t rows, int64_t stride, int64_t width, int e)
+{
+    return rows <= 1 || stride <= (INT64_MAX / e - width) / (rows - 1);
+}
+
 bool element_aligned(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (elt(dtype) - 1)) == 0; }
 
 }  // namespace
@@ -448,6 +454,8 @@ extern "C" bdssm_status bdssm_gated_norm(const bdssm_norm_dims *dims, const void
         return BDSSM_ERR_ALIGN;
     const int64_t n = dims->rows * dims->width;
     const int e = elt(dims->dtype);
+    if (!span_fits(dims->rows, z_stride, dims->width, e))
+        return BDSSM_ERR_UNSUPPORTED;
     const Range ro = rng(out, n * e), ry = rng(y, n * elt(dims->x_dtype));
     if (overlap(ro, rng(z, span(dims->rows, z_stride, dims->width, e))) || overlap(ro, rng(weight, dims->width * 4ll)) ||
         (overlap(ro, ry) && !(out == y && dims->dtype == dims->x_dtype)))
@@ -486,6 +494,8 @@ extern "C" bdssm_status bdssm_residual_norm(const bdssm_norm_dims *dims, const b
     const int64_t n = dims->rows * dims->width;
     const int e = elt(dims->dtype), xe = elt(dims->x_dtype);
     const int64_t streams = mod ? (dims->rows + dims->rows_per_stream - 1) / dims->rows_per_stream : 0;
+    if (!span_fits(streams, r->mod_stride, dims->width, e))
+        return BDSSM_ERR_UNSUPPORTED;
     const int64_t mb = span(streams, r->mod_stride, dims->width, e);
     const Range rx = rng(r->x, n * xe), rxo = rng(x_out, n * xe), ru = rng(u, n * e);
     for (Range q : {rxo, ru}) {

@@ -466,7 +466,8 @@ typedef struct {
  *   out     [rows][width] in dtype; may be y itself when the types are the same, must not
  *           overlap anything else
  * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (dtypes, kind, eps, more than
- * 16384 channels in a group), BDSSM_ERR_ALIGN, BDSSM_ERR_ALIAS, BDSSM_ERR_HIP.
+ * 16384 channels in a group, rows that reach past 64-bit addresses), BDSSM_ERR_ALIGN,
+ * BDSSM_ERR_ALIAS, BDSSM_ERR_HIP.
  */
 bdssm_status bdssm_gated_norm(const bdssm_norm_dims *dims, const void *y, const void *z, int64_t z_stride,
                               const float *weight, int32_t norm_first, void *out, void *stream);
