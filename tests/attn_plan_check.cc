@@ -42,6 +42,18 @@ int fail(const char *what, const Shape &s, int len, size_t have, size_t want)
     return 1;
 }
 
+bdssm_status call_step(const Shape &s, int len, size_t bytes)
+{
+    auto at = [](int i) { return reinterpret_cast<void *>((uintptr_t{1} << 45) + (static_cast<uintptr_t>(i) << 41)); };
+    const int64_t qw = static_cast<int64_t>(s.kv) * s.group * s.headdim, kw = static_cast<int64_t>(s.kv) * s.headdim;
+    const int pages = (len + 63) / 64;
+    const bdssm_attn_dims d = {s.batch, s.kv * s.group, s.kv, s.headdim, s.dtype, 64};
+    const bdssm_attn_mask m = {0.125f, s.block, s.window, s.sinks};
+    const bdssm_attn_chunk c = {at(0), at(1), at(2), qw, kw, kw, static_cast<int64_t>(s.batch) * s.tokens, nullptr, s.tokens};
+    const bdssm_kv_cache k = {at(3), at(4), static_cast<int32_t *>(at(5)), static_cast<int32_t *>(at(6)), 1, pages, len};
+    return bdssm_attn_step(&d, &c, &k, &m, at(7), at(8), bytes, nullptr);
+}
+
 int check(const Shape &s, int longest, int step)
 {
     size_t most = 0, before = 0;
@@ -52,6 +64,8 @@ int check(const Shape &s, int longest, int step)
         const size_t need = p.nsplit == 1 ? 0 : (rows * 8 + 255) / 256 * 256 + rows * s.headdim * 4;
         if (p.ws_bytes != need)
             return fail("a plan's need is not its partial rows", s, n, p.ws_bytes, need);
+        if (need > 0 && call_step(s, n, need - 1) != BDSSM_ERR_WORKSPACE)
+            return fail("a step takes a byte less than its plan needs", s, n, need - 1, need);
         most = std::max(most, need);
         const size_t q = query(s, n);
         if (q < most)
