@@ -81,6 +81,13 @@ int check(const Shape &s, int longest, int step)
 
 int main()
 {
+    // few units of many row tiles, dealt to the XCDs in parts and walked tile by tile (the launch of
+    // a prompt): shapes that tests on the GPU take for it
+    for (const Shape &s : {Shape{BDSSM_BF16, 64, 33, 1, 64, 33, 0, 0, 0}, Shape{BDSSM_BF16, 128, 33, 1, 64, 33, 32, 0, 0}}) {
+        const AttnPlan p = plan_of(s, 500);
+        if (p.sub < 2 || p.rt_fast || p.nsplit != 1)
+            return fail("not a prompt's launch", s, 500, p.sub, p.rt_fast);
+    }
     const Shape known[] = {
         {BDSSM_BF16, 64, 1, 8, 5, 32, 0, 0, 0},    {BDSSM_BF16, 64, 1, 4, 6, 32, 0, 0, 0},
         {BDSSM_BF16, 128, 2, 4, 5, 1024, 0, 0, 0}, {BDSSM_BF16, 64, 1, 4, 6, 1, 0, 0, 0},
