@@ -592,7 +592,8 @@ def _chunk(ad, block_len, q, k, v, starts):
 
 
 def attn_step_workspace(ad, block_len, max_len, mask):
-    """bdssm_attn_step_workspace (SIZE_MAX for arguments the call would reject)."""
+    """bdssm_attn_step_workspace: bytes that serve max_len and every smaller one (SIZE_MAX for
+    arguments the call would reject)."""
     return load().bdssm_attn_step_workspace(ctypes.byref(ad), block_len, max_len, ctypes.byref(mask))
 
 

@@ -42,9 +42,11 @@
 //  - many rows, headdim 128: the matrix cores (42 % busy) share the clock with the exponentials
 //    (34 %) and with LDS, whose operand reads take half as long as the products; 970 TFLOP/s
 //    (a prompt chunk of 8,192 on 8,192, 20 heads: 1.06 ms);
-//  - many rows, headdim 64: the vector unit (54 % busy, matrix cores 37 %), half of whose work is
-//    the exponentials; 880 TFLOP/s on equal streams, 740 on unequal ones (64 x 16-32K tokens,
-//    768 rows: 1.23 ms), where short row tiles leave wavefronts idle;
+//  - many rows, headdim 64: no unit alone (vector 54 % busy, half of it exponentials, matrix cores
+//    37 %, so that they take turns more than they overlap); copies and the wait for them before
+//    every tile are a quarter (1,323 us with them, 1,006 without); 880 TFLOP/s on equal streams,
+//    740 on unequal ones (64 x 16-32K tokens, 768 rows: 1.23 ms), where short row tiles leave
+//    wavefronts idle;
 //  - float32: the matrix cores, 100 to 125 TFLOP/s.
 // Eight wavefronts of 32 rows, four a SIMD at headdim 64, did better than four of 64 (half the
 // LDS reads, but nothing hides a wavefront's own exponentials: 1340 against 1020 us on the
@@ -801,7 +803,9 @@ void join(const AttnArgs &a, int nsplit, const float *part, const float2 *ml, hi
 // f(WM, WK, TK, WPE): the kernel shape for R rows per (stream, KV head): row blocks of 32 and key
 // parts of a workgroup, keys of a tile, wavefronts per SIMD.
 //  bf16   up to 64 rows: 2 x 2 (16 rows a head group, 8 streams of 32,768, headdim 128: 107 us,
-//         115 us as 8 x 1); more: 8 x 1 (128 rows, headdim 64: 62 us, 77 us as 2 x 2)
+//         115 us as 8 x 1); more: 8 x 1 (128 rows, headdim 64: 62 us, 77 us as 2 x 2). Up to 32 rows
+//         as 1 x 4 with tiles of 128 is no faster: 6 rows on 255 keys 8.4 us, 8.9 so, on 1,000 keys
+//         of headdim 128 12.1, 15.6 so, on 16,384 keys the same
 //  f32    up to 32 rows of headdim 64: 1 x 4 (32 rows, 8 streams of 4,096: 28 us, 32 us as 2 x 2,
 //         47 us as 4 x 1); up to 64 rows: 2 x 2 (64 rows: 34 us, 49 us as 4 x 1; headdim 128:
 //         58 us, 83 us); more: 4 x 1, whose products leave no room for more wavefronts
@@ -843,6 +847,10 @@ struct Planner {
     // may stand alone (32 x 6 rows on 1,032 keys: 26.7 us in ranges of four, 15.9). A second
     // launch costs as much as eight bf16 tiles (24 rows on 259 keys: 8.4 us whole, 11.7 in two).
     static constexpr int64_t kStart = f32 ? 2 : 3, kSplit = f32 ? 1 : 8;
+    // At most 64 ranges: with four KV heads or more these fill the GPU (131,072 keys of headdim 128,
+    // one token of 24 heads over 4: 49 us, 53 us with up to 128). A stream of one or two KV heads
+    // alone would take more: one token of 6 heads over 1 on 131,072 keys of headdim 64 33 us, 24 us
+    // with up to 128, 20 us with up to 256.
     static constexpr int kMostRanges = 64;
     const AttnArgs &a;
     int64_t R, units, slots;  // rows per unit, (stream, KV head) pairs, workgroups of an XCD at a time
