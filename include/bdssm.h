@@ -580,8 +580,9 @@ typedef struct {
  *   out       [tokens][nheads][headdim] in dtype; must not overlap anything
  *   workspace at least bdssm_attn_step_workspace(...) bytes for block_len, max_len and mask:
  *             partial results of a long cache that is split over workgroups. What the query
- *             says for one max_len serves every smaller one too (the same dims, block_len and
- *             mask), so that a decoding loop allocates once, for its longest cache
+ *             says for one max_len serves every smaller one too, so that a decoding loop
+ *             allocates once, for its longest cache. Other dims, another block_len (a smaller one
+ *             too) or mask may need more: ask for each
  * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (headdim, page_size, dtype),
  * BDSSM_ERR_ALIGN (base pointers and row strides to 16 bytes; table, lens and starts to 4),
  * BDSSM_ERR_ALIAS, BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The workspace query returns SIZE_MAX
