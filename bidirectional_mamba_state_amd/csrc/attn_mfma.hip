@@ -895,9 +895,9 @@ struct Planner {
         return static_cast<int64_t>(p.per_xcd) * p.nrt_sub;
     }
     // The lengths for which a unit's row tiles come longest first and end together: a prompt in
-    // order, and a window without order where most of a row tile's keys are ahead of it. With
-    // float32 the latter still gains from whole rounds (2 x 1,031 tokens of 16 heads, window 512:
-    // 152 us whole, 103 in two).
+    // order, and a window without order where most of a row tile's keys are ahead of it and the
+    // tiles take more than one round. With float32 the latter still gains from whole rounds (2 x
+    // 1,031 tokens of 16 heads, window 512: 152 us whole, 103 in two).
     struct Lengths {
         int64_t from, to;  // [from, to)
     };
@@ -905,7 +905,7 @@ struct Planner {
     {
         if (a.block)
             return {0, 2ll * a.block_len};
-        if (!f32 && a.window && 2 * back() < back() + ahead() + TK)
+        if (!f32 && a.window && per_xcd(1) > slots && 2 * back() < back() + ahead() + TK)
             return {std::max<int64_t>(0, 2 * back() + 1 - a.block_len), INT64_MAX};
         return {0, 0};
     }
