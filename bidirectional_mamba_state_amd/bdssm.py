@@ -29,7 +29,12 @@ EXPORTS = ("bdssm_abi_version", "bdssm_status_str", "bdssm_prefix_scan_workspace
            "bdssm_state_bf16_bytes", "bdssm_state_bf16", "bdssm_block_step_variant",
            "bdssm_commit_refresh",
            "bdssm_gated_norm", "bdssm_residual_norm",
-           "bdssm_attn_step_workspace", "bdssm_attn_step", "bdssm_kv_append")
+           "bdssm_attn_step_workspace", "bdssm_attn_step", "bdssm_kv_append",
+           "bdssm_attn_step_ex_workspace", "bdssm_attn_step_ex",
+           "bdssm_rotary_turns", "bdssm_rotary_step", "bdssm_rotary_append",
+           "bdssm_pages_workspace", "bdssm_pages_advance", "bdssm_pages_fork", "bdssm_pages_compact",
+           "bdssm_pages_copy")
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_BASE, ROTARY_PARTS = range(4)
 NORM_RMS, NORM_LAYER = 0, 1
 STATE_F32, STATE_OPS, STATE_BF16 = 0, 1, 2
 
@@ -99,6 +104,34 @@ class AttnChunk(ctypes.Structure):
 class AttnMask(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("block", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("sinks", ctypes.c_int32)]
+
+
+class AttnScoresPtrs(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p),
+                ("first", ctypes.c_void_p), ("last", ctypes.c_void_p)]
+
+
+class RotaryFreqs(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("trained", ctypes.c_int32), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class RotaryPtrs(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("turns", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class RotaryOut(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64)]
+
+
+class PagesDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class PagesPtrs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("uses", ctypes.c_void_p)]
 
 
 _lib = None
@@ -175,6 +208,27 @@ def load():
         lib.bdssm_attn_step.argtypes = [P(AttnDims), P(AttnChunk), P(KvCachePtrs), P(AttnMask), V, V, SZ, V]
         lib.bdssm_kv_append.restype = ctypes.c_int
         lib.bdssm_kv_append.argtypes = [P(AttnDims), P(AttnChunk), P(KvCachePtrs), V, V]
+        lib.bdssm_attn_step_ex_workspace.restype = SZ
+        lib.bdssm_attn_step_ex_workspace.argtypes = [P(AttnDims), I32, I32, P(AttnMask), P(AttnScoresPtrs)]
+        lib.bdssm_attn_step_ex.restype = ctypes.c_int
+        lib.bdssm_attn_step_ex.argtypes = [P(AttnDims), P(AttnChunk), P(KvCachePtrs), P(AttnMask), P(AttnScoresPtrs),
+                                           V, V, SZ, V]
+        lib.bdssm_rotary_turns.restype = ctypes.c_int
+        lib.bdssm_rotary_turns.argtypes = [P(RotaryFreqs), V]
+        lib.bdssm_rotary_step.restype = ctypes.c_int
+        lib.bdssm_rotary_step.argtypes = [P(AttnDims), P(AttnChunk), P(RotaryPtrs), V, P(RotaryOut), V]
+        lib.bdssm_rotary_append.restype = ctypes.c_int
+        lib.bdssm_rotary_append.argtypes = [P(AttnDims), P(AttnChunk), P(KvCachePtrs), P(RotaryPtrs), P(RotaryOut), V, V]
+        lib.bdssm_pages_workspace.restype = SZ
+        lib.bdssm_pages_workspace.argtypes = [P(PagesDims)]
+        lib.bdssm_pages_advance.restype = ctypes.c_int
+        lib.bdssm_pages_advance.argtypes = [P(PagesDims), P(PagesPtrs), V, I32, I32, I32, V, V, V, V, SZ, V]
+        lib.bdssm_pages_fork.restype = ctypes.c_int
+        lib.bdssm_pages_fork.argtypes = [P(PagesDims), P(PagesPtrs), V, V, V, V, V, V, V, SZ, V]
+        lib.bdssm_pages_compact.restype = ctypes.c_int
+        lib.bdssm_pages_compact.argtypes = [P(PagesDims), P(PagesPtrs), V, V, V, V, V, SZ, V]
+        lib.bdssm_pages_copy.restype = ctypes.c_int
+        lib.bdssm_pages_copy.argtypes = [P(AttnDims), P(KvCachePtrs), V, I32, V]
         _lib = lib
     return _lib
 
@@ -614,6 +668,174 @@ def kv_append(ad, block_len, k, v, cache, lens_out=None, starts=None, stream=Non
     ch = _chunk(ad, block_len, None, k, v, starts)
     _check(load().bdssm_kv_append(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(cache.ptrs), _ptr(lens_out),
                                   _stream(stream)))
+
+
+class AttnScores:
+    """What bdssm_attn_step_ex does to the scores and the mask: cap (0 = none), slopes [nheads]
+    float32 of the distance bias, prefix [batch] int32, and first, last [tokens] int32, the range of
+    keys of every chunk row; all but cap on the device, each or None. Keeps the tensors whose
+    addresses it holds; their contents may change between calls."""
+
+    def __init__(self, cap=0.0, slopes=None, prefix=None, first=None, last=None):
+        import torch
+        for t, what, dtype in ((slopes, "slopes", torch.float32), (prefix, "prefix", torch.int32),
+                               (first, "first", torch.int32), (last, "last", torch.int32)):
+            if t is not None and t.dtype != dtype:
+                raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+        self.slopes, self.prefix, self.first, self.last = slopes, prefix, first, last
+        self.ptrs = AttnScoresPtrs(cap, _ptr(slopes), _ptr(prefix), _ptr(first), _ptr(last))
+
+
+def attn_step_ex_workspace(ad, block_len, max_len, mask, scores):
+    """bdssm_attn_step_ex_workspace: bytes that serve max_len and every smaller one (SIZE_MAX for
+    arguments the call would reject)."""
+    return load().bdssm_attn_step_ex_workspace(ctypes.byref(ad), block_len, max_len, ctypes.byref(mask),
+                                               ctypes.byref(scores.ptrs))
+
+
+def attn_step_ex(ad, block_len, q, k, v, cache, mask, scores, out, workspace=None, starts=None, stream=None):
+    """bdssm_attn_step_ex: attn_step with the scores shaped and the rows' ranges limited by scores
+    (an AttnScores)."""
+    ch = _chunk(ad, block_len, q, k, v, starts)
+    _expect(out, "out", q.dtype, q.shape)
+    for t, what, n in ((scores.slopes, "slopes", ad.nheads), (scores.prefix, "prefix", ad.batch),
+                       (scores.first, "first", ch.tokens), (scores.last, "last", ch.tokens)):
+        if t is not None and t.shape != (n,):
+            raise ValueError(f"{what}: expected ({n},), got {tuple(t.shape)}")
+    _check(load().bdssm_attn_step_ex(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(cache.ptrs), ctypes.byref(mask),
+                                     ctypes.byref(scores.ptrs), _ptr(out), _ptr(workspace), _nbytes(workspace),
+                                     _stream(stream)))
+
+
+def rotary_turns(dim, base=10000.0, kind=ROTARY_PLAIN, factor=1.0, trained=0, low=1.0, high=32.0, device="cuda"):
+    """bdssm_rotary_turns: the frequencies of dim rotated channels as turns per position in units of
+    2^-64, [dim / 2] int64 (the bits of uint64) on the device."""
+    import torch
+    out = np.zeros(max(dim // 2, 1), dtype=np.uint64)
+    f = RotaryFreqs(dim, kind, base, factor, trained, low, high)
+    _check(load().bdssm_rotary_turns(ctypes.byref(f), out.ctypes.data))
+    return torch.from_numpy(out.view(np.int64)).to(device)
+
+
+class Rotary:
+    """A bdssm_rotary: turns (of rotary_turns; they say how many channels are rotated), the pairs'
+    layout and the scale. positions [tokens] int32 replaces the cache's own positions (None). Keeps
+    the tensors whose addresses it holds."""
+
+    def __init__(self, turns, interleaved=False, scale=1.0, positions=None):
+        import torch
+        _expect(turns, "turns", torch.int64, (turns.numel(),))
+        if positions is not None:
+            _expect(positions, "positions", torch.int32, (positions.numel(),))
+        self.turns, self.positions = turns, positions
+        self.ptrs = RotaryPtrs(2 * turns.numel(), int(interleaved), scale, _ptr(turns), _ptr(positions))
+
+
+def _rotary_out(ad, rotary, ch, q_out, k_out):
+    if rotary.positions is not None and rotary.positions.shape != (ch.tokens,):
+        raise ValueError(f"positions: expected ({ch.tokens},), got {tuple(rotary.positions.shape)}")
+    qp = kp = None
+    qs = ks = 0
+    dt, D = _torch_dtype(ad.dtype), ad.headdim
+    if q_out is not None:
+        qp, qs = _rows(q_out, "q_out", dt, (ch.tokens, ad.nheads, D))
+    if k_out is not None:
+        kp, ks = _rows(k_out, "k_out", dt, (ch.tokens, ad.kv_heads, D))
+    return RotaryOut(qp, kp, qs, ks)
+
+
+def rotary_step(ad, block_len, rotary, q, k, q_out, k_out, lens=None, starts=None, stream=None):
+    """bdssm_rotary_step: q [tokens, nheads, headdim] turned into q_out and k [tokens, kv_heads,
+    headdim] into k_out (q, k or other rows; each pair may be None); lens [batch] int32 or None."""
+    ch = _chunk(ad, block_len, q, k, None, starts)
+    out = _rotary_out(ad, rotary, ch, q_out, k_out)
+    if lens is not None:
+        import torch
+        _expect(lens, "lens", torch.int32, (ad.batch,))
+    _check(load().bdssm_rotary_step(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(rotary.ptrs), _ptr(lens),
+                                    ctypes.byref(out), _stream(stream)))
+
+
+def rotary_append(ad, block_len, rotary, q, k, v, cache, q_out, k_out=None, lens_out=None, starts=None, stream=None):
+    """bdssm_rotary_append: q turned into q_out, k turned into the cache's pages (and k_out), v into
+    the pages; lens_out [batch] int32 receives the new lengths. q = q_out = None: keys alone."""
+    if lens_out is not None:
+        _expect(lens_out, "lens_out", cache.lens.dtype, (ad.batch,))
+    ch = _chunk(ad, block_len, q, k, v, starts)
+    out = _rotary_out(ad, rotary, ch, q_out, k_out)
+    _check(load().bdssm_rotary_append(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(cache.ptrs),
+                                      ctypes.byref(rotary.ptrs), ctypes.byref(out), _ptr(lens_out), _stream(stream)))
+
+
+def page_dims(batch, page_size, num_pages, max_pages):
+    return PagesDims(batch, page_size, num_pages, max_pages)
+
+
+class Pages:
+    """A paged cache's bookkeeping as the pages_* calls take it: table [batch, max_pages], lens
+    [batch] and uses [num_pages], int32 on the device. Keeps the tensors whose addresses it holds;
+    their contents may change between calls."""
+
+    def __init__(self, pd, table, lens, uses):
+        import torch
+        _expect(table, "table", torch.int32, (pd.batch, pd.max_pages))
+        _expect(lens, "lens", torch.int32, (pd.batch,))
+        _expect(uses, "uses", torch.int32, (pd.num_pages,))
+        self.table, self.lens, self.uses = table, lens, uses
+        self.ptrs = PagesPtrs(_ptr(table), _ptr(lens), _ptr(uses))
+
+
+def _expect_ints(pairs):
+    import torch
+    for t, what, shape in pairs:
+        _expect(t, what, torch.int32, shape)
+
+
+def pages_workspace(pd):
+    """bdssm_pages_workspace: bytes that serve each of the pages_* calls (SIZE_MAX for dims that they
+    would reject)."""
+    return load().bdssm_pages_workspace(ctypes.byref(pd))
+
+
+def pages_advance(pd, pages, block_len, table_out, uses_out, lacking, workspace, window=0, sinks=0, starts=None,
+                  stream=None):
+    """bdssm_pages_advance: the pages of the next block_len tokens (or of starts) taken, those behind
+    the window given back; table_out and uses_out may be the pages' own; lacking [1] int32."""
+    _expect_ints(((table_out, "table_out", (pd.batch, pd.max_pages)), (uses_out, "uses_out", (pd.num_pages,)),
+                  (lacking, "lacking", (1,))))
+    if starts is not None:
+        _expect_ints(((starts, "starts", (pd.batch + 1,)),))
+    _check(load().bdssm_pages_advance(ctypes.byref(pd), ctypes.byref(pages.ptrs), _ptr(starts), block_len, window, sinks,
+                                      _ptr(table_out), _ptr(uses_out), _ptr(lacking), _ptr(workspace), _nbytes(workspace),
+                                      _stream(stream)))
+
+
+def pages_fork(pd, pages, parents, table_out, lens_out, uses_out, copies, lacking, workspace, stream=None):
+    """bdssm_pages_fork: row b becomes the stream of row parents[b] ([batch] int32); copies [batch, 2]
+    int32 receives the page copies to be made in every layer (pages_copy), lacking [1] int32."""
+    _expect_ints(((parents, "parents", (pd.batch,)), (table_out, "table_out", (pd.batch, pd.max_pages)),
+                  (lens_out, "lens_out", (pd.batch,)), (uses_out, "uses_out", (pd.num_pages,)),
+                  (copies, "copies", (pd.batch, 2)), (lacking, "lacking", (1,))))
+    _check(load().bdssm_pages_fork(ctypes.byref(pd), ctypes.byref(pages.ptrs), _ptr(parents), _ptr(table_out),
+                                   _ptr(lens_out), _ptr(uses_out), _ptr(copies), _ptr(lacking), _ptr(workspace),
+                                   _nbytes(workspace), _stream(stream)))
+
+
+def pages_compact(pd, pages, table_out, uses_out, copies, live, workspace, stream=None):
+    """bdssm_pages_compact: the used pages moved to the front of the pool; copies [num_pages // 2, 2]
+    int32 receives the moves to be made in every layer (pages_copy), live [1] int32 their number."""
+    _expect_ints(((table_out, "table_out", (pd.batch, pd.max_pages)), (uses_out, "uses_out", (pd.num_pages,)),
+                  (copies, "copies", (pd.num_pages // 2, 2)), (live, "live", (1,))))
+    _check(load().bdssm_pages_compact(ctypes.byref(pd), ctypes.byref(pages.ptrs), _ptr(table_out), _ptr(uses_out),
+                                      _ptr(copies), _ptr(live), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def pages_copy(ad, cache, copies, stream=None):
+    """bdssm_pages_copy: the pages of copies [n, 2] int32 (source, destination) copied within one
+    layer's pools (a KvCache)."""
+    _expect_ints(((copies, "copies", (copies.shape[0], 2)),))
+    _check(load().bdssm_pages_copy(ctypes.byref(ad), ctypes.byref(cache.ptrs), _ptr(copies), copies.shape[0],
+                                   _stream(stream)))
 
 
 # ------------------------------------------------------------------ data movement helpers

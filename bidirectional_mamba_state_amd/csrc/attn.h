@@ -3,8 +3,12 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <limits.h>
 
 #include <cstdint>
+
+#include "bdssm.h"
+#include "host_checks.h"
 
 namespace bdssm {
 
@@ -31,6 +35,15 @@ struct Divisor {
     __host__ __device__ __forceinline__ int rest(int n) const { return n - (*this)(n) * static_cast<int>(d); }
 };
 
+// Shaped scores and ranges of rows (bdssm_attn_scores), for bdssm_attn_step_ex.
+struct AttnScoring {
+    float x_per_score = 0.f;          // scale / cap
+    float cap_log2 = 0.f;             // cap log2 e; 0: no cap
+    const float *slopes = nullptr;    // [H]
+    const int *prefix = nullptr;      // [batch]
+    const int *first = nullptr, *last = nullptr;  // [tokens]
+};
+
 struct AttnArgs {
     const void *q, *k, *v;  // chunk rows; k, v NULL: no keys of its own
     int64_t q_stride, k_stride, v_stride;
@@ -45,6 +58,7 @@ struct AttnArgs {
     int block, window, sinks;
     Divisor by_block, by_group;  // block (1 where it is 0), H / KV
     void *out;
+    AttnScoring score;
 };
 
 // One stream's chunk rows and cached tokens. Every count read from device memory is brought
@@ -55,10 +69,9 @@ struct AttnStream {
     int len;       // cached tokens
 };
 
-__device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b)
+__device__ __forceinline__ AttnStream attn_rows(const AttnArgs &a, int b, int len)
 {
     AttnStream s;
-    const int len = a.lens[b];
     s.len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
     if (!a.starts) {
         s.row0 = static_cast<int64_t>(b) * a.block_len;
@@ -73,7 +86,25 @@ __device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b)
     return s;
 }
 
+__device__ __forceinline__ AttnStream attn_stream(const AttnArgs &a, int b) { return attn_rows(a, b, a.lens[b]); }
+
 constexpr int64_t kMaxGroups = (int64_t{1} << 32) / 512 - 1;  // a grid's threads have to fit 32 bits
+
+// ---- host: argument checks that the attention layer's entries share (attn.hip)
+
+// Positions and row numbers are 32-bit integers in the kernels, offsets inside eight rows too.
+constexpr int64_t kMaxPosition = INT_MAX - 1024, kMaxStride = 1 << 24;
+
+struct AttnRanges {
+    Range q, k, v, kp, vp, table, lens, starts;
+};
+
+bdssm_status check_attn_dims(const bdssm_attn_dims *d);
+
+// Checks dims, chunk and cache and fills the kernel arguments (mask and out are the caller's).
+// need_q: a step; need_kv: the chunk must bring keys and values.
+bdssm_status prepare_attn(const bdssm_attn_dims *d, const bdssm_attn_chunk *ch, const bdssm_kv_cache *ca, bool need_q,
+                          bool need_kv, AttnArgs *out, AttnRanges *r);
 
 // Launch plan of a step. A unit is one (stream, KV head, range of its keys); its row tiles read
 // the same keys, so they go to one XCD (its L2 then fetches them once), side by side in time.
@@ -95,5 +126,6 @@ AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);
 // rows than a launch has threads for.
 size_t attn_workspace(const AttnArgs &a, int D, bool bf16);
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
+hipError_t launch_attn_scored(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 
 }  // namespace bdssm

@@ -40,11 +40,10 @@ __global__ __launch_bounds__(256) void k_append(AttnArgs a, int *lens_out, int h
     static_cast<uint4 *>(a.vp)[to] = vx;
 }
 
-// Positions and row numbers are 32-bit integers in the kernels, offsets inside eight rows too.
-constexpr int64_t kMaxPosition = INT_MAX - 1024, kMaxStride = 1 << 24;
-
 // rows (token, head of a group) of a stream, and with them the grid's threads
 bool rows_fit(const AttnArgs &a) { return static_cast<int64_t>(a.block_len) * (a.H / a.KV) <= 1 << 30; }
+
+}  // namespace
 
 bdssm_status check_attn_dims(const bdssm_attn_dims *d)
 {
@@ -63,6 +62,8 @@ bdssm_status check_attn_dims(const bdssm_attn_dims *d)
     return BDSSM_OK;
 }
 
+namespace {
+
 bdssm_status check_attn_mask(const bdssm_attn_mask *m)
 {
     if (!m)
@@ -74,14 +75,8 @@ bdssm_status check_attn_mask(const bdssm_attn_mask *m)
     return BDSSM_OK;
 }
 
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
 
-struct AttnRanges {
-    Range q, k, v, kp, vp, table, lens, starts;
-};
-
-// Checks dims, chunk and cache and fills the kernel arguments (mask and out are the caller's).
-// need_q: a step; need_kv: the chunk must bring keys and values.
 bdssm_status prepare_attn(const bdssm_attn_dims *d, const bdssm_attn_chunk *ch, const bdssm_kv_cache *ca, bool need_q,
                           bool need_kv, AttnArgs *out, AttnRanges *r)
 {
@@ -136,6 +131,84 @@ bdssm_status prepare_attn(const bdssm_attn_dims *d, const bdssm_attn_chunk *ch, 
     return BDSSM_OK;
 }
 
+namespace {
+
+// Fills the scoring part of a step's arguments; the ranges that its output may not overlap follow.
+bdssm_status prepare_scores(const bdssm_attn_scores *s, float scale, AttnArgs *a, Range (&r)[4])
+{
+    if (!s)
+        return BDSSM_ERR_NULL;
+    if (!(s->cap >= 0.f) || s->cap - s->cap != 0.f)  // negative, NaN or infinite
+        return BDSSM_ERR_UNSUPPORTED;
+    if (!aligned4(s->slopes) || !aligned4(s->prefix) || !aligned4(s->first) || !aligned4(s->last))
+        return BDSSM_ERR_ALIGN;
+    AttnScoring &g = a->score;
+    if (s->cap > 0.f) {
+        const double log2e = 1.4426950408889634074;
+        g.x_per_score = static_cast<float>(static_cast<double>(scale) / s->cap);
+        g.cap_log2 = static_cast<float>(s->cap * log2e);
+        // both have to be ordinary numbers, or a score of zero would come out as none
+        const float least = 0x1p-126f, most = 0x1p126f;
+        if (!(g.x_per_score >= least && g.x_per_score <= most && g.cap_log2 >= least && g.cap_log2 <= most))
+            return BDSSM_ERR_UNSUPPORTED;
+    }
+    g.slopes = s->slopes, g.prefix = s->prefix, g.first = s->first, g.last = s->last;
+    r[0] = rng(s->slopes, a->H * 4ll);
+    r[1] = rng(s->prefix, a->batch * 4ll);
+    r[2] = rng(s->first, a->tokens * 4);
+    r[3] = rng(s->last, a->tokens * 4);
+    return BDSSM_OK;
+}
+
+bdssm_status attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_kv_cache *cache,
+                       const bdssm_attn_mask *mask, const bdssm_attn_scores *scores, bool scored, void *out, void *workspace,
+                       size_t workspace_bytes, void *stream)
+{
+    AttnArgs a;
+    AttnRanges r;
+    Range more[4] = {};
+    bdssm_status rc = prepare_attn(dims, chunk, cache, true, false, &a, &r);
+    if (rc != BDSSM_OK)
+        return rc;
+    if ((rc = check_attn_mask(mask)) != BDSSM_OK)
+        return rc;
+    if (scored && (rc = prepare_scores(scores, mask->scale, &a, more)) != BDSSM_OK)
+        return rc;
+    if (!out && a.tokens > 0)
+        return BDSSM_ERR_NULL;
+    if (!aligned(out) || !aligned(workspace))
+        return BDSSM_ERR_ALIGN;
+    const Range ro = rng(out, a.tokens * a.H * dims->headdim * elt(dims->dtype));
+    const Range in[] = {r.q, r.k, r.v, r.kp, r.vp, r.table, r.lens, r.starts, more[0], more[1], more[2], more[3]};
+    for (Range q : in)
+        if (overlap(ro, q))
+            return BDSSM_ERR_ALIAS;
+    if (a.batch == 0 || a.block_len == 0 || a.tokens == 0)
+        return BDSSM_OK;
+    a.scale = mask->scale, a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
+    a.by_block = Divisor(mask->block > 0 ? mask->block : 1);
+    a.by_group = Divisor(dims->nheads / dims->kv_heads);
+    a.out = out;
+    if (!rows_fit(a))
+        return BDSSM_ERR_UNSUPPORTED;
+    const bool bf16 = dims->dtype == BDSSM_BF16;
+    const AttnPlan p = attn_plan(a, dims->headdim, bf16);
+    if (p.groups > kMaxGroups)
+        return BDSSM_ERR_UNSUPPORTED;
+    if (p.ws_bytes > 0) {
+        if (!workspace || workspace_bytes < p.ws_bytes)
+            return BDSSM_ERR_WORKSPACE;
+        const Range rw = rng(workspace, static_cast<int64_t>(p.ws_bytes));
+        for (Range q : in)
+            if (overlap(rw, q))
+                return BDSSM_ERR_ALIAS;
+        if (overlap(rw, ro))
+            return BDSSM_ERR_ALIAS;
+    }
+    return launched((scored ? launch_attn_scored : launch_attn)(a, dims->headdim, bf16, p, workspace,
+                                                                static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace bdssm
 
@@ -158,46 +231,30 @@ extern "C" size_t bdssm_attn_step_workspace(const bdssm_attn_dims *dims, int32_t
     return attn_workspace(a, dims->headdim, dims->dtype == BDSSM_BF16);
 }
 
+extern "C" size_t bdssm_attn_step_ex_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len,
+                                               const bdssm_attn_mask *mask, const bdssm_attn_scores *scores)
+{
+    AttnArgs a{};
+    Range r[4];
+    if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK ||
+        prepare_scores(scores, mask->scale, &a, r) != BDSSM_OK)
+        return SIZE_MAX;
+    return bdssm_attn_step_workspace(dims, block_len, max_len, mask);
+}
+
 extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,
                                         const bdssm_kv_cache *cache, const bdssm_attn_mask *mask, void *out,
                                         void *workspace, size_t workspace_bytes, void *stream)
 {
-    AttnArgs a;
-    AttnRanges r;
-    bdssm_status rc = prepare_attn(dims, chunk, cache, true, false, &a, &r);
-    if (rc != BDSSM_OK)
-        return rc;
-    if ((rc = check_attn_mask(mask)) != BDSSM_OK)
-        return rc;
-    if (!out && a.tokens > 0)
-        return BDSSM_ERR_NULL;
-    if (!aligned(out) || !aligned(workspace))
-        return BDSSM_ERR_ALIGN;
-    const Range ro = rng(out, a.tokens * a.H * dims->headdim * elt(dims->dtype));
-    for (Range q : {r.q, r.k, r.v, r.kp, r.vp, r.table, r.lens, r.starts})
-        if (overlap(ro, q))
-            return BDSSM_ERR_ALIAS;
-    if (a.batch == 0 || a.block_len == 0 || a.tokens == 0)
-        return BDSSM_OK;
-    a.scale = mask->scale, a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
-    a.by_block = Divisor(mask->block > 0 ? mask->block : 1);
-    a.by_group = Divisor(dims->nheads / dims->kv_heads);
-    a.out = out;
-    if (!rows_fit(a))
-        return BDSSM_ERR_UNSUPPORTED;
-    const bool bf16 = dims->dtype == BDSSM_BF16;
-    const AttnPlan p = attn_plan(a, dims->headdim, bf16);
-    if (p.groups > kMaxGroups)
-        return BDSSM_ERR_UNSUPPORTED;
-    if (p.ws_bytes > 0) {
-        if (!workspace || workspace_bytes < p.ws_bytes)
-            return BDSSM_ERR_WORKSPACE;
-        const Range rw = rng(workspace, static_cast<int64_t>(p.ws_bytes));
-        for (Range q : {r.q, r.k, r.v, r.kp, r.vp, r.table, r.lens, r.starts, ro})
-            if (overlap(rw, q))
-                return BDSSM_ERR_ALIAS;
-    }
-    return launched(launch_attn(a, dims->headdim, bf16, p, workspace, static_cast<hipStream_t>(stream)));
+    return attn_step(dims, chunk, cache, mask, nullptr, false, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" bdssm_status bdssm_attn_step_ex(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,
+                                           const bdssm_kv_cache *cache, const bdssm_attn_mask *mask,
+                                           const bdssm_attn_scores *scores, void *out, void *workspace,
+                                           size_t workspace_bytes, void *stream)
+{
+    return attn_step(dims, chunk, cache, mask, scores, true, out, workspace, workspace_bytes, stream);
 }
 
 extern "C" bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,

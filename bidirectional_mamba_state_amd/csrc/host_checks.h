@@ -24,6 +24,8 @@ inline Range rng(const void *p, int64_t bytes)
 
 inline bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline int elt(int dtype) { return dtype == BDSSM_BF16 ? 2 : 4; }
 
 inline bdssm_status launched(hipError_t e) { return e == hipSuccess ? BDSSM_OK : BDSSM_ERR_HIP; }

@@ -1,0 +1,616 @@
+// Upkeep of a paged cache: taking and giving back pages (bdssm_pages_advance), forking streams
+// (bdssm_pages_fork), moving the used pages to the front (bdssm_pages_compact) and copying pages
+// (bdssm_pages_copy).
+//
+// The first three are three launches each. The first takes a snapshot of which pages are free, one
+// bit a page, with a count per chunk of the pool, and counts what each stream needs; the second
+// lists the free pages in order; in the third every stream finds its place among the needs (the sum
+// of those in front of it) and takes its pages from the list. Nothing is handed out by an atomic
+// counter, so that results depend on the contents alone; the uses of pages are counted by integer
+// atomics, whose sum has no order. The snapshot lets uses_out be uses itself.
+#include <limits.h>
+
+#include <algorithm>
+
+#include "attn.h"
+#include "internal.h"
+#include "wave_ops.h"
+
+namespace bdssm {
+namespace {
+
+constexpr int kWords = 64;            // words of 64 pages that a workgroup takes of the pool,
+constexpr int kChunk = 64 * kWords;   // and so many pages
+
+struct PoolArgs {
+    const int *table, *lens, *uses;
+    int *table_out, *uses_out;
+    int batch, page_shift, num_pages, max_pages, chunks, row_parts;
+    // workspace
+    uint64_t *bits;  // [chunks][kWords]: the page is free
+    int *counts;     // [chunks] free pages
+    int *needs;      // [batch]
+    int *list;       // [num_pages] free pages in order
+    int *map;        // [num_pages] compact: which move a page is, or -1
+    int *moves;      // [1] compact: number of moves
+};
+
+// sum over a workgroup of 256 threads, in every thread
+__device__ __forceinline__ int block_sum(int v, int *lds)
+{
+#pragma unroll
+    for (int y = 1; y < 64; y *= 2)
+        v += __shfl_xor(v, y);
+    __syncthreads();  // lds may still be read from an earlier sum
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return lds[0] + lds[1] + lds[2] + lds[3];
+}
+
+// sum of v[0 .. n), by a workgroup
+__device__ __forceinline__ int sum_of(const int *v, int n, int *lds)
+{
+    int s = 0;
+    for (int i = threadIdx.x; i < n; i += 256)
+        s += v[i];
+    return block_sum(s, lds);
+}
+
+// A chunk of the snapshot, and uses as they go on being counted (none below 0).
+__device__ __forceinline__ void snapshot(const PoolArgs &a, int chunk, int *lds)
+{
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int n = 0;
+    for (int i = w; i < kWords; i += 4) {
+        const int64_t p = static_cast<int64_t>(chunk) * kChunk + 64 * i + lane;
+        const int u = p < a.num_pages ? a.uses[p] : 1;
+        const uint64_t word = __ballot(u <= 0);
+        if (p < a.num_pages && (u < 0 || a.uses_out != a.uses))
+            a.uses_out[p] = u > 0 ? u : 0;
+        if (lane == 0)
+            a.bits[static_cast<int64_t>(chunk) * kWords + i] = word;
+        n += __popcll(word);  // the same in every lane
+    }
+    const int all = block_sum(lane == 0 ? n : 0, lds);
+    if (threadIdx.x == 0)
+        a.counts[chunk] = all;
+}
+
+__device__ __forceinline__ int cached(const PoolArgs &a, int b)
+{
+    const int64_t held = static_cast<int64_t>(a.max_pages) << a.page_shift;
+    const int len = a.lens[b];
+    return len < 0 ? 0 : len > held ? static_cast<int>(held) : len;
+}
+
+__device__ __forceinline__ bool is_page(const PoolArgs &a, int e) { return e >= 0 && e < a.num_pages; }
+
+// ---- advance
+struct AdvanceArgs {
+    PoolArgs p;
+    const int *starts;
+    int block_len, window, sinks;
+    int *lacking;
+};
+
+struct Span {
+    int from, to;  // entries that a stream's new tokens start: from the first page at or past its length
+    int len;
+};
+
+__device__ __forceinline__ Span new_entries(const AdvanceArgs &a, int b)
+{
+    const int len = cached(a.p, b), page = 1 << a.p.page_shift;
+    int64_t n = a.block_len;
+    if (a.starts) {
+        n = static_cast<int64_t>(a.starts[b + 1]) - a.starts[b];
+        n = n < 0 ? 0 : n > a.block_len ? a.block_len : n;
+    }
+    const int64_t held = static_cast<int64_t>(a.p.max_pages) << a.p.page_shift;
+    const int64_t end = len + n < held ? len + n : held;
+    return Span{static_cast<int>((static_cast<int64_t>(len) + page - 1) >> a.p.page_shift),
+                static_cast<int>((end + page - 1) >> a.p.page_shift), len};
+}
+
+// empty entries among [from, to) of a row, by a workgroup
+__device__ __forceinline__ int empty_entries(const PoolArgs &a, const int *row, int from, int to, int *lds)
+{
+    int n = 0;
+    for (int i = from + threadIdx.x; i < to; i += 256)
+        n += !is_page(a, row[i]);
+    return block_sum(n, lds);
+}
+
+__global__ __launch_bounds__(256) void k_advance_count(AdvanceArgs a)
+{
+    __shared__ int lds[4];
+    if (static_cast<int>(blockIdx.x) < a.p.chunks)
+        return snapshot(a.p, blockIdx.x, lds);
+    const int b = blockIdx.x - a.p.chunks;
+    const Span s = new_entries(a, b);
+    const int n = empty_entries(a.p, a.p.table + static_cast<int64_t>(b) * a.p.max_pages, s.from, s.to, lds);
+    if (threadIdx.x == 0)
+        a.p.needs[b] = n;
+}
+
+// Free pages of a chunk into the list.
+__global__ __launch_bounds__(256) void k_list(PoolArgs a)
+{
+    __shared__ int lds[4];
+    const int chunk = blockIdx.x, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int rank = sum_of(a.counts, chunk, lds);
+    for (int i = 0; i < kWords; ++i) {
+        const uint64_t word = a.bits[static_cast<int64_t>(chunk) * kWords + i];
+        if ((i & 3) == w && (word >> lane & 1))
+            a.list[rank + __popcll(word & ((uint64_t{1} << lane) - 1))] = chunk * kChunk + 64 * i + lane;
+        rank += __popcll(word);
+    }
+}
+
+// A row's part [from, to) of `parts`.
+__device__ __forceinline__ Span part_of(const PoolArgs &a, int part)
+{
+    const int per = (a.max_pages + a.row_parts - 1) / a.row_parts;
+    const int64_t from = static_cast<int64_t>(part) * per;
+    return Span{static_cast<int>(from < a.max_pages ? from : a.max_pages),
+                static_cast<int>(from + per < a.max_pages ? from + per : a.max_pages), 0};
+}
+
+// Rows, a part of one each: gives back, takes, counts. The entries that new tokens start are the
+// first part's, so that none is ranked by a table that another workgroup has begun to fill.
+__global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
+{
+    __shared__ int lds[4];
+    const int b = blockIdx.y, page = 1 << a.p.page_shift, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    if (b >= a.p.batch) {  // no streams
+        if (threadIdx.x == 0)
+            a.lacking[0] = 0;
+        return;
+    }
+    const int64_t row = static_cast<int64_t>(b) * a.p.max_pages;
+    const int *in = a.p.table + row;
+    int *out = a.p.table_out + row;
+    const Span s = new_entries(a, b), part = part_of(a.p, blockIdx.x);
+    for (int i = part.from + threadIdx.x; i < part.to; i += 256) {
+        if (i >= s.from && i < s.to)
+            continue;
+        const int e = in[i];
+        const int64_t at = static_cast<int64_t>(i) << a.p.page_shift;
+        // the next query is at position len and looks back to len - window + 1
+        const bool seen = a.window == 0 || at < a.sinks || at + page > static_cast<int64_t>(s.len) - a.window + 1;
+        const bool kept = i < s.from && seen && is_page(a.p, e);
+        if (!kept && is_page(a.p, e))
+            atomicSub(&a.p.uses_out[e], 1);
+        if (in != out || !kept)
+            out[i] = kept ? e : -1;
+    }
+    if (blockIdx.x != 0)
+        return;
+    const int free = sum_of(a.p.counts, a.p.chunks, lds);
+    if (b == 0) {
+        const int need = sum_of(a.p.needs, a.p.batch, lds);
+        if (threadIdx.x == 0)
+            a.lacking[0] = need > free ? need - free : 0;
+    }
+    if (s.from >= s.to)
+        return;
+    int place = sum_of(a.p.needs, b, lds);
+    for (int i0 = s.from; i0 < s.to; i0 += 256) {
+        const int i = i0 + threadIdx.x;
+        const int e = i < s.to ? in[i] : 0;
+        const bool empty = i < s.to && !is_page(a.p, e);
+        const uint64_t word = __ballot(empty);
+        __syncthreads();
+        if (lane == 0)
+            lds[w] = __popcll(word);
+        __syncthreads();
+        int r = place + __popcll(word & ((uint64_t{1} << lane) - 1));
+        for (int x = 0; x < w; ++x)
+            r += lds[x];
+        place += lds[0] + lds[1] + lds[2] + lds[3];
+        if (empty) {
+            const int e_new = r < free ? a.p.list[r] : -1;
+            if (e_new >= 0)
+                atomicAdd(&a.p.uses_out[e_new], 1);
+            out[i] = e_new;
+        } else if (i < s.to && in != out) {
+            out[i] = e;
+        }
+    }
+}
+
+// ---- fork
+struct ForkArgs {
+    PoolArgs p;
+    const int *parents;
+    int *lens_out, *copies, *lacking;
+    int *again;  // workspace [batch]: an earlier row has the same parent
+};
+
+__global__ __launch_bounds__(256) void k_fork_count(ForkArgs a)
+{
+    __shared__ int lds[4];
+    if (static_cast<int>(blockIdx.x) < a.p.chunks)
+        return snapshot(a.p, blockIdx.x, lds);
+    const int b = (blockIdx.x - a.p.chunks) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;  // a wavefront per row
+    if (b >= a.p.batch)
+        return;
+    const int parent = a.parents[b];
+    int again = 0, need = 0;
+    if (parent >= 0 && parent < a.p.batch) {
+        for (int i0 = 0; i0 < b && !again; i0 += 64)
+            again = __ballot(i0 + lane < b && a.parents[i0 + lane < b ? i0 + lane : 0] == parent) != 0;
+        const int len = cached(a.p, parent), part = len & ((1 << a.p.page_shift) - 1);
+        need = again && part && is_page(a.p, a.p.table[static_cast<int64_t>(parent) * a.p.max_pages + (len >> a.p.page_shift)]);
+    }
+    if (lane == 0) {
+        a.again[b] = again;
+        a.p.needs[b] = need;
+    }
+}
+
+__global__ __launch_bounds__(256) void k_fork_rows(ForkArgs a)
+{
+    __shared__ int lds[4];
+    if (a.p.batch == 0) {
+        if (threadIdx.x == 0)
+            a.lacking[0] = 0;
+        return;
+    }
+    const int b = blockIdx.y, parent = a.parents[b], again = a.again[b], need = a.p.needs[b];
+    const bool goes_on = parent >= 0 && parent < a.p.batch;
+    const int len = goes_on ? cached(a.p, parent) : 0, whole = len >> a.p.page_shift;
+    const Span part = part_of(a.p, blockIdx.x);
+    const int *from = a.p.table + static_cast<int64_t>(goes_on ? parent : 0) * a.p.max_pages;
+    const int64_t row = static_cast<int64_t>(b) * a.p.max_pages;
+    int fresh = -1;
+    if (blockIdx.x == 0 || (need && whole >= part.from && whole < part.to)) {
+        const int free = sum_of(a.p.counts, a.p.chunks, lds);
+        if (need) {
+            const int place = sum_of(a.p.needs, b, lds);
+            fresh = place < free ? a.p.list[place] : -1;
+        }
+        if (blockIdx.x == 0) {
+            const int all = b == 0 ? sum_of(a.p.needs, a.p.batch, lds) : 0;
+            if (threadIdx.x == 0) {
+                if (b == 0)
+                    a.lacking[0] = all > free ? all - free : 0;
+                a.lens_out[b] = len;
+                a.copies[2 * static_cast<int64_t>(b)] = fresh >= 0 ? from[whole] : -1;
+                a.copies[2 * static_cast<int64_t>(b) + 1] = fresh;
+            }
+        }
+    }
+    for (int i = part.from + threadIdx.x; i < part.to; i += 256) {
+        int e = goes_on && !(again && i >= whole) ? from[i] : -1;
+        if (need && i == whole)
+            e = fresh;
+        e = is_page(a.p, e) ? e : -1;
+        const int old = a.p.table[row + i];
+        if (e != old) {
+            if (e >= 0)
+                atomicAdd(&a.p.uses_out[e], 1);
+            if (is_page(a.p, old))
+                atomicSub(&a.p.uses_out[old], 1);
+        }
+        a.p.table_out[row + i] = e;
+    }
+}
+
+// ---- compact
+struct CompactArgs {
+    PoolArgs p;
+    int *copies, *live;
+};
+
+__global__ __launch_bounds__(256) void k_snapshot(PoolArgs a)
+{
+    __shared__ int lds[4];
+    snapshot(a, blockIdx.x, lds);
+}
+
+// Of n used pages: the free pages below n into the list, in order; the move number of the used ones
+// from n on, the highest first; how many there are (the free pages in front of page n).
+__global__ __launch_bounds__(256) void k_compact_list(CompactArgs a)
+{
+    __shared__ int lds[4];
+    const int chunk = blockIdx.x, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int live = a.p.num_pages - sum_of(a.p.counts, a.p.chunks, lds);
+    if (a.p.num_pages == 0) {
+        if (threadIdx.x == 0)
+            a.live[0] = 0;
+        return;
+    }
+    int rank = sum_of(a.p.counts, chunk, lds);  // free pages in front of the word's
+    if (chunk == 0 && threadIdx.x == 0) {
+        a.live[0] = live;
+        if (live == a.p.num_pages)
+            a.p.moves[0] = 0;
+    }
+    for (int i = 0; i < kWords; ++i) {
+        const uint64_t word = a.p.bits[static_cast<int64_t>(chunk) * kWords + i];
+        const int64_t p = static_cast<int64_t>(chunk) * kChunk + 64 * i + lane;
+        if ((i & 3) == w && p < a.p.num_pages) {
+            const int before = rank + __popcll(word & ((uint64_t{1} << lane) - 1));
+            const bool free = word >> lane & 1;
+            if (p >= live)
+                a.p.map[p] = free ? -1 : live - 1 - (static_cast<int>(p) - before);
+            else if (free)
+                a.p.list[before] = static_cast<int>(p);
+            if (p == live)
+                a.p.moves[0] = before;
+        }
+        rank += __popcll(word);
+    }
+}
+
+__global__ __launch_bounds__(256) void k_compact_move(CompactArgs a)
+{
+    __shared__ int lds[4];
+    const int live = a.p.num_pages - sum_of(a.p.counts, a.p.chunks, lds);
+    if (static_cast<int>(blockIdx.x) < a.p.chunks) {
+        const int moves = a.p.moves[0], most = a.p.num_pages / 2;
+        for (int x = threadIdx.x; x < kChunk; x += 256) {
+            const int64_t p = static_cast<int64_t>(blockIdx.x) * kChunk + x;
+            if (p >= moves && p < most)
+                a.copies[2 * p] = a.copies[2 * p + 1] = -1;
+            if (p < live || p >= a.p.num_pages)
+                continue;
+            const int r = a.p.map[p];
+            if (r < 0)
+                continue;
+            const int to = a.p.list[r];
+            a.p.uses_out[to] = a.p.uses_out[p];
+            a.p.uses_out[p] = 0;
+            a.copies[2 * static_cast<int64_t>(r)] = static_cast<int>(p);
+            a.copies[2 * static_cast<int64_t>(r) + 1] = to;
+        }
+        return;
+    }
+    const int64_t all = static_cast<int64_t>(a.p.batch) * a.p.max_pages;
+    const int64_t step = static_cast<int64_t>(gridDim.x - a.p.chunks) * 256;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x - a.p.chunks) * 256 + threadIdx.x; i < all; i += step) {
+        const int e = a.p.table[i];
+        int to = is_page(a.p, e) ? e : -1;
+        if (to >= live) {
+            const int r = a.p.map[e];
+            to = r < 0 ? e : a.p.list[r];
+        }
+        if (to != e || a.p.table_out != a.p.table)
+            a.p.table_out[i] = to;
+    }
+}
+
+// ---- copies
+// A workgroup takes 16 KB of a page of one pool: entries along x, pools and parts along y.
+constexpr int kPieces = 4;  // 16-byte pieces of a thread
+
+__global__ __launch_bounds__(256) void k_pages_copy(char *k, char *v, const int *copies, int n, int num_pages, int64_t page_bytes)
+{
+    char *pool = blockIdx.y & 1 ? v : k;
+    const int64_t at = (static_cast<int64_t>(blockIdx.y >> 1) * kPieces * 256 + threadIdx.x) * 16;
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        const int2 c = make_int2(copies[2 * static_cast<int64_t>(i)], copies[2 * static_cast<int64_t>(i) + 1]);
+        if (c.x < 0 || c.y < 0 || c.x >= num_pages || c.y >= num_pages || c.x == c.y)
+            continue;
+        const char *from = pool + c.x * page_bytes;
+        char *to = pool + c.y * page_bytes;
+        uint4 d[kPieces];
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x)
+            if (at + x * 4096 < page_bytes)
+                d[x] = *reinterpret_cast<const uint4 *>(from + at + x * 4096);
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x)
+            if (at + x * 4096 < page_bytes)
+                *reinterpret_cast<uint4 *>(to + at + x * 4096) = d[x];
+    }
+}
+
+// ---- host
+bdssm_status check_pages_dims(const bdssm_pages_dims *d)
+{
+    if (!d)
+        return BDSSM_ERR_NULL;
+    if (d->batch < 0 || d->num_pages < 0 || d->max_pages < 0)
+        return BDSSM_ERR_SHAPE;
+    const int p = d->page_size;
+    if ((p != 16 && p != 32 && p != 64 && p != 128 && p != 256) || d->batch > 65535 ||
+        static_cast<int64_t>(d->max_pages) * p > kMaxPosition)
+        return BDSSM_ERR_UNSUPPORTED;
+    return BDSSM_OK;
+}
+
+int64_t chunks_of(const bdssm_pages_dims *d) { return (static_cast<int64_t>(d->num_pages) + kChunk - 1) / kChunk; }
+
+// Bytes of the workspace, and with `a` and `again` the places in it.
+size_t workspace_of(const bdssm_pages_dims *d, char *ws, PoolArgs *a, int **again)
+{
+    int64_t used = 0;
+    auto take = [&](int64_t bytes) {
+        char *at = ws ? ws + used : nullptr;
+        used += (bytes + 15) / 16 * 16;
+        return at;
+    };
+    PoolArgs none;
+    int *skip;
+    a = a ? a : &none, again = again ? again : &skip;
+    a->bits = reinterpret_cast<uint64_t *>(take(chunks_of(d) * kWords * 8));
+    a->counts = reinterpret_cast<int *>(take(chunks_of(d) * 4));
+    a->needs = reinterpret_cast<int *>(take(d->batch * 4ll));
+    *again = reinterpret_cast<int *>(take(d->batch * 4ll));
+    a->list = reinterpret_cast<int *>(take(d->num_pages * 4ll));
+    a->map = reinterpret_cast<int *>(take(d->num_pages * 4ll));
+    a->moves = reinterpret_cast<int *>(take(4));
+    return static_cast<size_t>(used);
+}
+
+// What the three calls check alike: pointers, alignment, overlaps (of the inputs in `in`, the outputs
+// in `out`; the first output is table_out, the second uses_out, which may be in place), workspace.
+bdssm_status prepare_pages(const bdssm_pages_dims *d, const bdssm_pages *g, const int32_t *extra_in, int64_t extra_count,
+                           bool need_extra, int32_t *const (&out)[5], const int64_t (&count)[5], bool table_in_place,
+                           void *ws, size_t ws_bytes, PoolArgs *a, int **again)
+{
+    const bdssm_status rc = check_pages_dims(d);
+    if (rc != BDSSM_OK)
+        return rc;
+    if (!g)
+        return BDSSM_ERR_NULL;
+    const int64_t entries = static_cast<int64_t>(d->batch) * d->max_pages;
+    const Range in[4] = {rng(g->table, entries * 4), rng(g->uses, d->num_pages * 4ll), rng(g->lens, d->batch * 4ll),
+                         rng(extra_in, extra_count * 4)};
+    if ((!g->table && entries > 0) || (!g->uses && d->num_pages > 0) || (!g->lens && d->batch > 0) ||
+        (need_extra && !extra_in && extra_count > 0))
+        return BDSSM_ERR_NULL;
+    for (int i = 0; i < 5; ++i)
+        if (!out[i] && count[i] > 0)
+            return BDSSM_ERR_NULL;
+    if (!aligned4(g->table) || !aligned4(g->uses) || !aligned4(g->lens) || !aligned4(extra_in) || !aligned(ws))
+        return BDSSM_ERR_ALIGN;
+    for (int i = 0; i < 5; ++i)
+        if (!aligned4(out[i]))
+            return BDSSM_ERR_ALIGN;
+    for (int i = 0; i < 5; ++i) {
+        const Range w = rng(out[i], count[i] * 4);
+        for (int j = 0; j < 4; ++j) {
+            const bool in_place = i == j && (i == 1 || (i == 0 && table_in_place)) && w.lo == in[j].lo;
+            if (!in_place && overlap(w, in[j]))
+                return BDSSM_ERR_ALIAS;
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(w, rng(out[j], count[j] * 4)))
+                return BDSSM_ERR_ALIAS;
+    }
+    *a = PoolArgs{};
+    const size_t need = workspace_of(d, static_cast<char *>(ws), a, again);
+    if (!ws || ws_bytes < need)
+        return BDSSM_ERR_WORKSPACE;
+    const Range rw = rng(ws, static_cast<int64_t>(need));
+    for (const Range &x : in)
+        if (overlap(rw, x))
+            return BDSSM_ERR_ALIAS;
+    for (int i = 0; i < 5; ++i)
+        if (overlap(rw, rng(out[i], count[i] * 4)))
+            return BDSSM_ERR_ALIAS;
+    a->table = g->table, a->lens = g->lens, a->uses = g->uses;
+    a->table_out = out[0], a->uses_out = out[1];
+    a->batch = d->batch, a->page_shift = __builtin_ctz(d->page_size);
+    a->num_pages = d->num_pages, a->max_pages = d->max_pages;
+    a->chunks = static_cast<int>(chunks_of(d));
+    // parts of a row: a thousand entries or more each, as many as fill the GPU
+    a->row_parts = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>((d->max_pages + 1023) / 1024, 1024 / std::max(1, d->batch))));
+    return BDSSM_OK;
+}
+
+}  // namespace
+}  // namespace bdssm
+
+using namespace bdssm;
+
+extern "C" size_t bdssm_pages_workspace(const bdssm_pages_dims *dims)
+{
+    return check_pages_dims(dims) == BDSSM_OK ? workspace_of(dims, nullptr, nullptr, nullptr) : SIZE_MAX;
+}
+
+extern "C" bdssm_status bdssm_pages_advance(const bdssm_pages_dims *dims, const bdssm_pages *pages, const int32_t *starts,
+                                            int32_t block_len, int32_t window, int32_t sinks, int32_t *table_out,
+                                            int32_t *uses_out, int32_t *lacking, void *workspace, size_t workspace_bytes,
+                                            void *stream)
+{
+    AdvanceArgs a{};
+    int *again;
+    const int64_t batch = dims ? dims->batch : 0;
+    int32_t *const out[5] = {table_out, uses_out, lacking, nullptr, nullptr};
+    const int64_t count[5] = {dims ? batch * dims->max_pages : 0, dims ? dims->num_pages : 0, 1, 0, 0};
+    const bdssm_status rc = prepare_pages(dims, pages, starts, batch + 1, false, out, count, true, workspace,
+                                          workspace_bytes, &a.p, &again);
+    if (rc != BDSSM_OK)
+        return rc;
+    if (block_len < 0 || window < 0 || sinks < 0)
+        return BDSSM_ERR_SHAPE;
+    a.starts = starts, a.block_len = block_len, a.window = window, a.sinks = sinks, a.lacking = lacking;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (a.p.chunks + dims->batch > 0)
+        k_advance_count<<<a.p.chunks + dims->batch, 256, 0, st>>>(a);
+    if (a.p.chunks > 0)
+        k_list<<<a.p.chunks, 256, 0, st>>>(a.p);
+    k_advance_rows<<<dim3(a.p.row_parts, std::max(1, dims->batch)), 256, 0, st>>>(a);
+    return launched(hipGetLastError());
+}
+
+extern "C" bdssm_status bdssm_pages_fork(const bdssm_pages_dims *dims, const bdssm_pages *pages, const int32_t *parents,
+                                         int32_t *table_out, int32_t *lens_out, int32_t *uses_out, int32_t *copies,
+                                         int32_t *lacking, void *workspace, size_t workspace_bytes, void *stream)
+{
+    ForkArgs a{};
+    const int64_t batch = dims ? dims->batch : 0;
+    int32_t *const out[5] = {table_out, uses_out, lens_out, copies, lacking};
+    const int64_t count[5] = {dims ? batch * dims->max_pages : 0, dims ? dims->num_pages : 0, batch, 2 * batch, 1};
+    const bdssm_status rc = prepare_pages(dims, pages, parents, batch, true, out, count, false, workspace, workspace_bytes,
+                                          &a.p, &a.again);
+    if (rc != BDSSM_OK)
+        return rc;
+    a.parents = parents, a.lens_out = lens_out, a.copies = copies, a.lacking = lacking;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int rows = (dims->batch + 3) / 4;
+    if (a.p.chunks + rows > 0)
+        k_fork_count<<<a.p.chunks + rows, 256, 0, st>>>(a);
+    if (a.p.chunks > 0)
+        k_list<<<a.p.chunks, 256, 0, st>>>(a.p);
+    k_fork_rows<<<dim3(a.p.row_parts, std::max(1, dims->batch)), 256, 0, st>>>(a);
+    return launched(hipGetLastError());
+}
+
+extern "C" bdssm_status bdssm_pages_compact(const bdssm_pages_dims *dims, const bdssm_pages *pages, int32_t *table_out,
+                                            int32_t *uses_out, int32_t *copies, int32_t *live, void *workspace,
+                                            size_t workspace_bytes, void *stream)
+{
+    CompactArgs a{};
+    int *again;
+    const int64_t entries = dims ? static_cast<int64_t>(dims->batch) * dims->max_pages : 0;
+    int32_t *const out[5] = {table_out, uses_out, copies, live, nullptr};
+    const int64_t count[5] = {entries, dims ? dims->num_pages : 0, dims ? dims->num_pages / 2 * 2ll : 0, 1, 0};
+    const bdssm_status rc = prepare_pages(dims, pages, nullptr, 0, false, out, count, true, workspace, workspace_bytes, &a.p,
+                                          &again);
+    if (rc != BDSSM_OK)
+        return rc;
+    a.copies = copies, a.live = live;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (a.p.chunks > 0)
+        k_snapshot<<<a.p.chunks, 256, 0, st>>>(a.p);
+    k_compact_list<<<std::max(1, a.p.chunks), 256, 0, st>>>(a);
+    const int rows = static_cast<int>(std::min<int64_t>(1024, (entries + 1023) / 1024));
+    if (a.p.chunks + rows > 0)
+        k_compact_move<<<a.p.chunks + rows, 256, 0, st>>>(a);
+    return launched(hipGetLastError());
+}
+
+extern "C" bdssm_status bdssm_pages_copy(const bdssm_attn_dims *dims, const bdssm_kv_cache *cache, const int32_t *copies,
+                                         int32_t n, void *stream)
+{
+    const bdssm_status rc = check_attn_dims(dims);
+    if (rc != BDSSM_OK)
+        return rc;
+    if (!cache)
+        return BDSSM_ERR_NULL;
+    if (cache->num_pages < 0 || n < 0)
+        return BDSSM_ERR_SHAPE;
+    if ((n > 0 && !copies) || (cache->num_pages > 0 && (!cache->k || !cache->v)))
+        return BDSSM_ERR_NULL;
+    if (!aligned4(copies) || !aligned(cache->k) || !aligned(cache->v))
+        return BDSSM_ERR_ALIGN;
+    const int64_t page_bytes = static_cast<int64_t>(dims->kv_heads) * dims->page_size * dims->headdim * elt(dims->dtype);
+    const Range k = rng(cache->k, cache->num_pages * page_bytes), v = rng(cache->v, cache->num_pages * page_bytes);
+    const Range rc_ = rng(copies, n * 8ll);
+    if (overlap(k, v) || overlap(rc_, k) || overlap(rc_, v))
+        return BDSSM_ERR_ALIAS;
+    if (n == 0 || cache->num_pages == 0)
+        return BDSSM_OK;
+    const int64_t parts = 2 * ((page_bytes + kPieces * 4096 - 1) / (kPieces * 4096));  // 8,192 for the largest page
+    const int64_t lists = std::min<int64_t>(n, std::max<int64_t>(1, 16384 / parts));
+    k_pages_copy<<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(parts)), 256, 0, static_cast<hipStream_t>(stream)>>>(
+        static_cast<char *>(cache->k), static_cast<char *>(cache->v), copies, n, cache->num_pages, page_bytes);
+    return launched(hipGetLastError());
+}

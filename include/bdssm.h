@@ -606,6 +606,207 @@ bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk
                              int32_t *lens_out, void *stream);
 
 /*
+ * Attention with shaped scores or ranges of each token's own: bdssm_attn_step (its layouts, mask,
+ * sums and roundings) whose score of query head h at position p with key j becomes
+ *     s = scale * q.k                                  (mask->scale)
+ *     s = cap * tanh(s / cap)                          where cap > 0
+ *     s = s - slopes[h] * |p - j|                      where slopes is given
+ * and whose mask becomes
+ *     order:   as bdssm_attn_step, or j < prefix[b]    (the first prefix[b] positions of stream b
+ *              are visible to each of its queries: a prompt that sees itself whole)
+ *     window:  as bdssm_attn_step (it limits a prefix too)
+ *     range:   first[i] <= j < last[i] for chunk row i, sinks included (the borders of the
+ *              token's document, as positions of its stream; first >= last: the token attends
+ *              to nothing, and gets zeros)
+ * Positions outside the stream's keys are taken as their nearest end. Distances are exact up to
+ * 2^24 and count from the nearest position that the query's window, order and range leave.
+ * Workgroups skip keys that the ranges of all their rows leave out, so that documents packed
+ * into one chunk cost what they cost apart.
+ *   cap       0 (none) or > 0, finite
+ *   slopes    [nheads] device float32, or NULL
+ *   prefix    [batch] device int32, or NULL
+ *   first, last  [tokens] device int32 in the order of chunk rows, each or NULL (0, no end)
+ * Errors as bdssm_attn_step; BDSSM_ERR_UNSUPPORTED also for a cap that is negative or not finite,
+ * or for which scale / cap or cap itself is beyond 2^-126 to 2^126 or so. out and workspace must
+ * not overlap these arrays. bdssm_attn_step_ex_workspace says what the call needs as
+ * bdssm_attn_step_workspace does (of scores, only cap is looked at).
+ */
+typedef struct {
+    float cap;
+    const float *slopes;
+    const int32_t *prefix;
+    const int32_t *first, *last;
+} bdssm_attn_scores;
+size_t bdssm_attn_step_ex_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len,
+                                    const bdssm_attn_mask *mask, const bdssm_attn_scores *scores);
+bdssm_status bdssm_attn_step_ex(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_kv_cache *cache,
+                                const bdssm_attn_mask *mask, const bdssm_attn_scores *scores, void *out,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions: in each head the channels of a pair (a, b) are turned by the angle t of the
+ * token's position and the pair's frequency f_i (radians per position),
+ *     a' = scale (a cos t - b sin t),  b' = scale (a sin t + b cos t),   t = position * f_i
+ * for pairs i < dim / 2 of channels (i, i + dim / 2), or (2i, 2i + 1) where interleaved; channels
+ * from dim on are taken over as they are. Frequencies come as turns per position in units of
+ * 2^-64, so that a position's angle, whole turns left out, is one wrapping integer product: it is
+ * off by |position| 2^-65 turns at most, at any position. Sines and cosines are float32 with an
+ * error of a few 2^-24, and so are products and sums, rounded once to dtype.
+ *
+ * bdssm_rotary_turns fills such a table on the host (copied to the device once, by the caller):
+ *     f_i = base^(-2i / dim)                                     BDSSM_ROTARY_PLAIN
+ *     f_i / factor                                               BDSSM_ROTARY_LINEAR
+ *     the same of base factor^(dim / (dim - 2))                  BDSSM_ROTARY_BASE  (dim > 2: the
+ *         lowest frequency is divided by factor, the highest is kept)
+ *     f_i (g + (1 - g) / factor)                                 BDSSM_ROTARY_PARTS
+ *         g = (r - low) / (high - low) within 0 and 1, r = trained f_i / (2 pi): pairs that make
+ *         more than `high` turns within the trained length are kept, those with fewer than `low`
+ *         are divided by factor
+ *   turns   [dim / 2] host, written
+ * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE (dim odd, below 2 or above 512), BDSSM_ERR_UNSUPPORTED
+ * (kind; base < 1, factor <= 0 or not finite; BASE with dim 2; PARTS with trained < 1 or
+ * low >= high).
+ */
+enum { BDSSM_ROTARY_PLAIN = 0, BDSSM_ROTARY_LINEAR = 1, BDSSM_ROTARY_BASE = 2, BDSSM_ROTARY_PARTS = 3 };
+typedef struct {
+    int32_t dim;     /* rotated channels of a head */
+    int32_t kind;
+    double base;     /* e.g. 10000 */
+    double factor;   /* how much longer than trained (ignored by PLAIN) */
+    int32_t trained; /* PARTS: tokens of the contexts trained on */
+    double low, high; /* PARTS: turns */
+} bdssm_rotary_freqs;
+bdssm_status bdssm_rotary_turns(const bdssm_rotary_freqs *freqs, uint64_t *turns);
+
+typedef struct {
+    int32_t dim;              /* rotated channels: even, 2 .. headdim */
+    int32_t interleaved;      /* 0 or 1 */
+    float scale;              /* of the rotated channels: 1, or a long context's factor; finite */
+    const uint64_t *turns;    /* [dim / 2] device, 8-byte aligned */
+    const int32_t *positions; /* [tokens] device, one for each chunk row (any value, negative ones
+                                 too), or NULL: chunk token i of stream b is at lens[b] + i */
+} bdssm_rotary;
+
+typedef struct {
+    void *q, *k;                /* first rows of [nheads][headdim] and of [kv_heads][headdim] */
+    int64_t q_stride, k_stride; /* elements between rows, as in bdssm_attn_chunk */
+} bdssm_rotary_out;
+
+/*
+ * Turns the chunk's queries and keys (each may be NULL with its output, not both; the chunk's v
+ * is not used).
+ *   lens   [batch] device: cached tokens, or NULL for none; below 0 taken as 0 (not read when
+ *          positions are given)
+ *   out    rows out->q, out->k: the chunk's own rows in place (same address and stride), or rows
+ *          that overlap nothing. Slices of the same projection rows do not overlap.
+ * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED, BDSSM_ERR_ALIGN, BDSSM_ERR_ALIAS,
+ * BDSSM_ERR_HIP, as bdssm_attn_step.
+ */
+bdssm_status bdssm_rotary_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_rotary *rotary,
+                               const int32_t *lens, const bdssm_rotary_out *out, void *stream);
+
+/*
+ * The same on the way into the cache: queries to out->q, keys turned into the pages (and to
+ * out->k where it is given), values into the pages, in one launch: bdssm_rotary_step followed by
+ * bdssm_kv_append of its keys. The positions of the turn are the cache's own (lens[b] + i, lens
+ * taken within 0 and max_len) unless rotary->positions gives others; the slots are the append's.
+ *   chunk->q with out->q   both NULL: keys alone
+ *   out      may be NULL when there are no queries
+ *   lens_out as in bdssm_kv_append
+ */
+bdssm_status bdssm_rotary_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_kv_cache *cache,
+                                 const bdssm_rotary *rotary, const bdssm_rotary_out *out, int32_t *lens_out, void *stream);
+
+/*
+ * Upkeep of a paged cache on the device, without a host round trip, so that a decoding loop that
+ * takes, shares and gives back pages can be recorded as a graph. What the attention layers of a
+ * stack share is one table and one pool's bookkeeping:
+ *   table  [batch][max_pages]  as in bdssm_kv_cache; entries outside [0, num_pages) hold nothing
+ *   lens   [batch]             cached tokens, taken within 0 and max_pages * page_size
+ *   uses   [num_pages]         table entries that name a page; 0 (or less): the page is free
+ * Pages are given out lowest number first, to streams in order, and a page that a call gives back
+ * is free from the next call on: results depend on the contents alone. Integer atomics count the
+ * uses, in whose order nothing depends.
+ *   table_out, uses_out   may be table and uses themselves (in place) except for the fork's
+ *                         table_out; else must not overlap anything
+ *   workspace             at least bdssm_pages_workspace(dims) bytes (the same for all calls),
+ *                         16-byte aligned; two calls that may run at the same time need one each
+ * A whole page may be shared: a stream's length is not to be lowered into one and written again.
+ * No call reads a count that the host does not have: where pages run out, the entries that lack
+ * one stay empty (-1) and lacking[0] says how many.
+ * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (page_size, batch above 65535,
+ * positions past 2^31), BDSSM_ERR_ALIGN (4 bytes; workspace 16), BDSSM_ERR_ALIAS,
+ * BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The query returns SIZE_MAX for dims the calls reject.
+ */
+typedef struct {
+    int32_t batch;     /* streams */
+    int32_t page_size; /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t num_pages; /* pages of the pool */
+    int32_t max_pages; /* entries of a table row */
+} bdssm_pages_dims;
+
+typedef struct {
+    const int32_t *table, *lens, *uses;
+} bdssm_pages;
+
+size_t bdssm_pages_workspace(const bdssm_pages_dims *dims);
+
+/*
+ * Before a block is decoded (or appended): afterwards every stream holds the pages of its tokens
+ * [0, lens[b] + n_b), n_b its new tokens, that a later query can see, and no others. Pages wholly
+ * behind the window (and past the sinks) and pages wholly past the new tokens are given back;
+ * entries from the first page that starts at lens[b] or later are filled with free pages. An empty
+ * entry among cached tokens stays empty.
+ *   starts     [batch + 1] device, as in bdssm_attn_chunk, or NULL: block_len tokens each
+ *   block_len  new tokens of a stream, or the most of any
+ *   window, sinks  as in bdssm_attn_mask
+ *   lacking    [1] device: entries that found no free page
+ */
+bdssm_status bdssm_pages_advance(const bdssm_pages_dims *dims, const bdssm_pages *pages, const int32_t *starts,
+                                 int32_t block_len, int32_t window, int32_t sinks, int32_t *table_out,
+                                 int32_t *uses_out, int32_t *lacking, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/*
+ * Streams rearranged, forked and ended: row b becomes the stream of row parents[b] (itself, if it
+ * goes on). Streams with one parent share its whole pages; the first of them keeps its last,
+ * partly filled page and what is held past it, each other one takes a free page for a copy of the
+ * partly filled one. So pages that are still written have one user. A parent outside [0, batch)
+ * leaves the row empty, and a row that no one descends from gives its pages back.
+ *   parents    [batch] device
+ *   table_out  must not overlap table;  lens_out [batch], must not overlap lens
+ *   copies     [batch][2] device, written: (source, destination) for row b, or (-1, -1): the page
+ *              copies to be made, in every layer's pools, by bdssm_pages_copy
+ *   lacking    [1] device: copies that found no free page (the entry stays empty)
+ */
+bdssm_status bdssm_pages_fork(const bdssm_pages_dims *dims, const bdssm_pages *pages, const int32_t *parents,
+                              int32_t *table_out, int32_t *lens_out, int32_t *uses_out, int32_t *copies,
+                              int32_t *lacking, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Moves the used pages to the front of the pool: of n used pages, those numbered n or above go to
+ * the free pages below n, the highest to the lowest. Afterwards exactly pages 0 to n - 1 are used.
+ *   copies  [num_pages / 2][2] device, written: (source, destination) of the moves, then (-1, -1)
+ *   live    [1] device: n
+ */
+bdssm_status bdssm_pages_compact(const bdssm_pages_dims *dims, const bdssm_pages *pages, int32_t *table_out,
+                                 int32_t *uses_out, int32_t *copies, int32_t *live, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * Copies pages within one layer's pools (keys and values), as a fork's or a compaction's list says:
+ * to be called for every layer, before the pages are read or given out again.
+ *   cache   k, v and num_pages are used
+ *   copies  [n][2] device (source, destination). Entries with a page outside the pool, and copies
+ *           of a page to itself, are left out. No destination may be another entry's source or
+ *           destination (a list that a fork or a compaction wrote never has one): what such a page
+ *           holds afterwards is not defined.
+ * Errors as bdssm_kv_append.
+ */
+bdssm_status bdssm_pages_copy(const bdssm_attn_dims *dims, const bdssm_kv_cache *cache, const int32_t *copies, int32_t n,
+                              void *stream);
+
+/*
  * Launch-shape override, for tests and launch-shape sweeps only (not for the hot path).
  * Several kernels implement the block step, each one in full and each checked against the
  * same bounds; the library picks one per call from the shapes. This call pins that choice
