@@ -134,17 +134,31 @@ __global__ __launch_bounds__(256) void k_advance_count(AdvanceArgs a)
         a.p.needs[b] = n;
 }
 
+// Lane l: the free pages in front of word l of a chunk (a word a lane), after those in front of it.
+__device__ __forceinline__ int words_before(uint64_t word, int before)
+{
+    const int own = __popcll(word);
+    int n = own;
+#pragma unroll
+    for (int y = 1; y < 64; y *= 2) {
+        const int o = __shfl_up(n, y);
+        n += static_cast<int>(threadIdx.x & 63) >= y ? o : 0;
+    }
+    return before + n - own;
+}
+
 // Free pages of a chunk into the list.
 __global__ __launch_bounds__(256) void k_list(PoolArgs a)
 {
     __shared__ int lds[4];
     const int chunk = blockIdx.x, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int rank = sum_of(a.counts, chunk, lds);
-    for (int i = 0; i < kWords; ++i) {
-        const uint64_t word = a.bits[static_cast<int64_t>(chunk) * kWords + i];
-        if ((i & 3) == w && (word >> lane & 1))
+    const uint64_t mine = a.bits[static_cast<int64_t>(chunk) * kWords + lane];
+    const int ranks = words_before(mine, sum_of(a.counts, chunk, lds));
+    for (int i = w; i < kWords; i += 4) {
+        const uint64_t word = __shfl(mine, i);
+        const int rank = __shfl(ranks, i);
+        if (word >> lane & 1)
             a.list[rank + __popcll(word & ((uint64_t{1} << lane) - 1))] = chunk * kChunk + 64 * i + lane;
-        rank += __popcll(word);
     }
 }
 
@@ -322,16 +336,18 @@ __global__ __launch_bounds__(256) void k_compact_list(CompactArgs a)
             a.live[0] = 0;
         return;
     }
-    int rank = sum_of(a.p.counts, chunk, lds);  // free pages in front of the word's
+    const uint64_t mine = a.p.bits[static_cast<int64_t>(chunk) * kWords + lane];
+    const int ranks = words_before(mine, sum_of(a.p.counts, chunk, lds));
     if (chunk == 0 && threadIdx.x == 0) {
         a.live[0] = live;
         if (live == a.p.num_pages)
             a.p.moves[0] = 0;
     }
-    for (int i = 0; i < kWords; ++i) {
-        const uint64_t word = a.p.bits[static_cast<int64_t>(chunk) * kWords + i];
+    for (int i = w; i < kWords; i += 4) {
+        const uint64_t word = __shfl(mine, i);
         const int64_t p = static_cast<int64_t>(chunk) * kChunk + 64 * i + lane;
-        if ((i & 3) == w && p < a.p.num_pages) {
+        const int rank = __shfl(ranks, i);
+        if (p < a.p.num_pages) {
             const int before = rank + __popcll(word & ((uint64_t{1} << lane) - 1));
             const bool free = word >> lane & 1;
             if (p >= live)
@@ -341,7 +357,6 @@ __global__ __launch_bounds__(256) void k_compact_list(CompactArgs a)
             if (p == live)
                 a.p.moves[0] = before;
         }
-        rank += __popcll(word);
     }
 }
 
@@ -383,28 +398,33 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a)
 }
 
 // ---- copies
-// A workgroup takes 16 KB of a page of one pool: entries along x, pools and parts along y.
+// A workgroup takes 16 KB of a page of one pool: entries along x, pools and parts along y. Threads
+// past the page's end read its last piece again, so that no load is conditional: a conditional one
+// per piece made the compiler keep the pieces in LDS and wait for each (800 pages of 32 KB: 25.7 us,
+// and 16 us for a list that names none).
 constexpr int kPieces = 4;  // 16-byte pieces of a thread
 
-__global__ __launch_bounds__(256) void k_pages_copy(char *k, char *v, const int *copies, int n, int num_pages, int64_t page_bytes)
+__global__ __launch_bounds__(256) void k_pages_copy(char *k, char *v, const int *copies, int n, int step, int num_pages,
+                                                    int64_t page_bytes)
 {
     char *pool = blockIdx.y & 1 ? v : k;
     const int64_t at = (static_cast<int64_t>(blockIdx.y >> 1) * kPieces * 256 + threadIdx.x) * 16;
-    for (int i = blockIdx.x; i < n; i += gridDim.x) {
-        const int2 c = make_int2(copies[2 * static_cast<int64_t>(i)], copies[2 * static_cast<int64_t>(i) + 1]);
-        if (c.x < 0 || c.y < 0 || c.x >= num_pages || c.y >= num_pages || c.x == c.y)
+    for (int i = blockIdx.x; i < n; i += step) {
+        const int from = copies[2 * static_cast<int64_t>(i)], to = copies[2 * static_cast<int64_t>(i) + 1];
+        if (from < 0 || to < 0 || from >= num_pages || to >= num_pages || from == to)
             continue;
-        const char *from = pool + c.x * page_bytes;
-        char *to = pool + c.y * page_bytes;
-        uint4 d[kPieces];
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x)
+        const char *src = pool + from * page_bytes;
+        char *dst = pool + to * page_bytes;
+        auto read = [&](int x) {
+            const int64_t o = at + x * 4096;
+            return *reinterpret_cast<const uint4 *>(src + (o < page_bytes ? o : page_bytes - 16));
+        };
+        const uint4 d0 = read(0), d1 = read(1), d2 = read(2), d3 = read(3);
+        auto write = [&](int x, uint4 d) {
             if (at + x * 4096 < page_bytes)
-                d[x] = *reinterpret_cast<const uint4 *>(from + at + x * 4096);
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x)
-            if (at + x * 4096 < page_bytes)
-                *reinterpret_cast<uint4 *>(to + at + x * 4096) = d[x];
+                *reinterpret_cast<uint4 *>(dst + at + x * 4096) = d;
+        };
+        write(0, d0), write(1, d1), write(2, d2), write(3, d3);
     }
 }
 
@@ -611,6 +631,6 @@ extern "C" bdssm_status bdssm_pages_copy(const bdssm_attn_dims *dims, const bdss
     const int64_t parts = 2 * ((page_bytes + kPieces * 4096 - 1) / (kPieces * 4096));  // 8,192 for the largest page
     const int64_t lists = std::min<int64_t>(n, std::max<int64_t>(1, 16384 / parts));
     k_pages_copy<<<dim3(static_cast<unsigned>(lists), static_cast<unsigned>(parts)), 256, 0, static_cast<hipStream_t>(stream)>>>(
-        static_cast<char *>(cache->k), static_cast<char *>(cache->v), copies, n, cache->num_pages, page_bytes);
+        static_cast<char *>(cache->k), static_cast<char *>(cache->v), copies, n, static_cast<int>(lists), cache->num_pages, page_bytes);
     return launched(hipGetLastError());
 }
