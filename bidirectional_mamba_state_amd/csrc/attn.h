@@ -39,6 +39,10 @@ struct Divisor {
 struct AttnScoring {
     float x_per_score = 0.f;          // scale / cap
     float cap_log2 = 0.f;             // cap log2 e; 0: no cap
+    float two_x_log2 = 0.f;           // 2 x_per_score log2 e
+    float half_cap = 0.f;             // the score (before scale) that is half of the cap
+    float q[4] = {};                  // polynomial of small scores, see attn_kernel.h
+    int fast = 0;                     // by the tile: bf16, a cap of 256 or less
     const float *slopes = nullptr;    // [H]
     const int *prefix = nullptr;      // [batch]
     const int *first = nullptr, *last = nullptr;  // [tokens]
@@ -126,6 +130,7 @@ AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);
 // rows than a launch has threads for.
 size_t attn_workspace(const AttnArgs &a, int D, bool bf16);
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
-hipError_t launch_attn_scored(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
+hipError_t launch_attn_ranged(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
+hipError_t launch_attn_capped(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 
 }  // namespace bdssm

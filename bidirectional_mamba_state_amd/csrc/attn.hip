@@ -134,7 +134,7 @@ bdssm_status prepare_attn(const bdssm_attn_dims *d, const bdssm_attn_chunk *ch, 
 namespace {
 
 // Fills the scoring part of a step's arguments; the ranges that its output may not overlap follow.
-bdssm_status prepare_scores(const bdssm_attn_scores *s, float scale, AttnArgs *a, Range (&r)[4])
+bdssm_status prepare_scores(const bdssm_attn_scores *s, float scale, bool bf16, AttnArgs *a, Range (&r)[4])
 {
     if (!s)
         return BDSSM_ERR_NULL;
@@ -151,6 +151,16 @@ bdssm_status prepare_scores(const bdssm_attn_scores *s, float scale, AttnArgs *a
         const float least = 0x1p-126f, most = 0x1p126f;
         if (!(g.x_per_score >= least && g.x_per_score <= most && g.cap_log2 >= least && g.cap_log2 <= most))
             return BDSSM_ERR_UNSUPPORTED;
+        const double x = static_cast<double>(scale) / s->cap;
+        g.two_x_log2 = static_cast<float>(2 * x * log2e);
+        g.half_cap = static_cast<float>(0.5 / x);
+        // tanh(x) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) up to 1/2, in powers of two of the raw score. Its
+        // terms stay ordinary numbers for any x from 2^-12 to 2^12 per score
+        const double c[4] = {0.999999456, -0.333263179, 0.131902966, -0.0444022263};
+        double power = s->cap * log2e * x;
+        for (int i = 0; i < 4; ++i, power *= x * x)
+            g.q[i] = static_cast<float>(c[i] * power);
+        g.fast = bf16 && s->cap <= 256.f && x >= 0x1p-12 && x <= 0x1p12;
     }
     g.slopes = s->slopes, g.prefix = s->prefix, g.first = s->first, g.last = s->last;
     r[0] = rng(s->slopes, a->H * 4ll);
@@ -172,7 +182,7 @@ bdssm_status attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chun
         return rc;
     if ((rc = check_attn_mask(mask)) != BDSSM_OK)
         return rc;
-    if (scored && (rc = prepare_scores(scores, mask->scale, &a, more)) != BDSSM_OK)
+    if (scored && (rc = prepare_scores(scores, mask->scale, dims->dtype == BDSSM_BF16, &a, more)) != BDSSM_OK)
         return rc;
     if (!out && a.tokens > 0)
         return BDSSM_ERR_NULL;
@@ -205,8 +215,8 @@ bdssm_status attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chun
         if (overlap(rw, ro))
             return BDSSM_ERR_ALIAS;
     }
-    return launched((scored ? launch_attn_scored : launch_attn)(a, dims->headdim, bf16, p, workspace,
-                                                                static_cast<hipStream_t>(stream)));
+    const auto launch = !scored ? launch_attn : a.score.cap_log2 > 0.f ? launch_attn_capped : launch_attn_ranged;
+    return launched(launch(a, dims->headdim, bf16, p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -237,7 +247,7 @@ extern "C" size_t bdssm_attn_step_ex_workspace(const bdssm_attn_dims *dims, int3
     AttnArgs a{};
     Range r[4];
     if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK ||
-        prepare_scores(scores, mask->scale, &a, r) != BDSSM_OK)
+        prepare_scores(scores, mask->scale, dims->dtype == BDSSM_BF16, &a, r) != BDSSM_OK)
         return SIZE_MAX;
     return bdssm_attn_step_workspace(dims, block_len, max_len, mask);
 }

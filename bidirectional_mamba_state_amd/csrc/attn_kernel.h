@@ -197,27 +197,52 @@ __device__ __forceinline__ int prefix_of(const AttnArgs &a, int b, int end)
     return v < 0 ? 0 : v > end ? end : v;
 }
 
-// Shaped scores (in powers of two, before the maximum).
+// What a kernel does to scores and ranges beyond the mask of bdssm_attn_step: nothing; ranges of rows and
+// a bias, each where it is given (AttnArgs::score); a cap, and those.
+enum Mode { kPlain, kRanged, kCapped };
+
+// Shaped scores, in powers of two.
 //
-// Cap: c tanh(x), x = s / c. From |x| = 0.6 on tanh x = 1 - 2 / (1 + e^2x), whose rounding is a few
-// 2^-24 of a result above 0.53, and which an infinite score takes to +-1; below, where it would
-// cancel, the series up to x^17 (the next term is 3 2^-27 of x at 0.6). So the cap's own error is a
-// few 2^-24 of the score, whatever the cap.
+// Cap: c tanh(x), x = s / c. Two forms: x Q(x^2), Q the polynomial with the least relative error up to
+// some |x|; and 1 - 2 / (1 + e^2x), whose error is a few 2^-24 of c, and which an infinite score takes
+// to +-1. Each costs: the polynomial a multiplication and an addition a term, the other two
+// transcendentals, which take as long as eight additions.
+//  - Exactly (float32, or a cap above 256): six terms up to 0.6 (2.5e-9), the other form from there on,
+//    where it is a few 2^-24 of the score too.
+//  - For bf16 (see AttnScoring::fast): by the tile. Where a wavefront sees a whole tile and all of its
+//    scores are below c / 2, four terms (5.4e-7 of the score: up to 1e-4 of a power of two, a fortieth
+//    of the rounding of a bf16 weight), made along with the weights, where the products hide them; else
+//    the other form for all (a few 2^-24 of c).
 __device__ __forceinline__ float capped(float s, const AttnScoring &g)
 {
     const float x = s * g.x_per_score, u = x * x;
-    float t = 6404582.f / 10854718875.f;
-    t = fmaf(t, u, -929569.f / 638512875.f);
-    t = fmaf(t, u, 21844.f / 6081075.f);
-    t = fmaf(t, u, -1382.f / 155925.f);
-    t = fmaf(t, u, 62.f / 2835.f);
-    t = fmaf(t, u, -17.f / 315.f);
-    t = fmaf(t, u, 2.f / 15.f);
-    t = fmaf(t, u, -1.f / 3.f);
+    float t = -0.00585216868f;
+    t = fmaf(t, u, 0.020753629f);
+    t = fmaf(t, u, -0.0537687048f);
+    t = fmaf(t, u, 0.13331689f);
+    t = fmaf(t, u, -0.333332833f);
     t = fmaf(t * u, x, x);
-    const float e = __builtin_amdgcn_exp2f(x * (2.f * kLog2e));
-    return g.cap_log2 * (u < 0.36f ? t : fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + e), 1.f));
+    float far = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e))), 1.f);
+    asm("" : "+v"(far));  // both, then one of the two: no branch around each score
+    return g.cap_log2 * (u < 0.36f ? t : far);
 }
+// any scores, to a few 2^-24 of c
+__device__ __forceinline__ float capped_any(float s, const AttnScoring &g)
+{
+    const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s * g.two_x_log2));
+    return fmaf(r, -2.f * g.cap_log2, g.cap_log2);
+}
+// The polynomial of a tile: that of small scores, or 1 where the scores are shaped already.
+struct Poly {
+    float q0, q1, q2, q3;
+    __device__ __forceinline__ float operator()(float s) const
+    {
+        const float u = s * s;
+        return fmaf(u, fmaf(u, fmaf(u, q3, q2), q1), q0);
+    }
+};
+// A score that is not attended to where Poly makes the weights: its square is finite, its power of two 0.
+constexpr float kHidden = -0x1p60f;
 
 // Bias: a slope times the distance to the key. The softmax does not change when a row's scores
 // move together, so the distance is taken from the nearest position that the row attends to
@@ -235,11 +260,12 @@ __device__ __forceinline__ int bias_from(const Sight &x, int p)
 // (Looking through the values of tiles that rows see in part, before use, cost 2 to 6 % of every
 // call; this costs nothing measurable until it is needed, and much then: a NaN among the last
 // values of a prompt of 8,192 tokens on 8,192, 1.1 ms to 196 ms, which is one workgroup's 256 rows.)
-template <typename T, int D, bool EX>
-__device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional_t<EX, RowRangeEx, RowRange> &in_lds, int *found,
+template <typename T, int D, int MODE>
+__device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional_t<MODE != kPlain, RowRangeEx, RowRange> &in_lds, int *found,
                                        float *part, float2 *part_ml)
 {
     const auto x = in_lds;
+    constexpr bool EX = MODE != kPlain;
     constexpr int EL = sizeof(T), ROWB = D * EL, PPR = ROWB / 16, PL = D / 64;  // PL: channels of a lane
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, G = static_cast<int>(a.by_group.d);
     const AttnStream s = attn_stream(a, x.b);
@@ -305,7 +331,7 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional
                     for (int c = 0; c < D; ++c)
                         sj = fmaf(static_cast<float>(q[c]), static_cast<float>(k[c]), sj);
                 if constexpr (EX) {
-                    sj = a.score.cap_log2 > 0.f ? capped(sj, a.score) : sj * (a.scale * kLog2e);
+                    sj = MODE == kCapped ? capped(sj, a.score) : sj * (a.scale * kLog2e);
                     if (a.score.slopes)
                         sj = fmaf(-slope, fabsf(static_cast<float>(bias_from(see, s.len + tok) - j)), sj);
                 }
@@ -355,8 +381,7 @@ struct AttnCfg {
     static constexpr int TILE_BYTES = TK * Tile<T, D>::ROWB;
 };
 
-// EX: scores are shaped (cap, bias), or rows have ranges of their own (AttnArgs::score).
-template <typename T, int D, int WM, int WK, int TK, int WPE, bool EX>
+template <typename T, int D, int WM, int WK, int TK, int WPE, int MODE>
 __global__ __launch_bounds__((AttnCfg<T, D, WM, WK, TK>::THREADS))
 __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan pl, float *part, float2 *part_ml)
 {
@@ -369,6 +394,12 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     constexpr int PIDS = (TK + 63) / 64;            // 64-key words of a tile's key mask
     constexpr int KB = TK / 32 / WK;                // 32-key blocks of a wavefront per tile
     constexpr int EL = sizeof(T);
+    constexpr bool EX = MODE != kPlain;
+    // Whether `raise` and `weigh` find raw scores, to be scaled: a bias is then what the products start
+    // from. float32 adds it up in up to 64 products, each with its rounding, so there it comes after.
+    constexpr bool RAW = MODE == kPlain || (MODE == kRanged && EL == 2);
+    constexpr bool POLY = MODE == kCapped && EL == 2;  // weights are made by a tile's polynomial
+    constexpr bool SCHED = MODE != kPlain && EL == 2;  // the order of LDS reads and products is given
     constexpr uint64_t kAll = TK < 64 ? 0xffffffffull : ~0ull;  // a mask of keys with all of them
     static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0, "tile shape");
 
@@ -571,9 +602,9 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
 
     f32x16 o[D / 32] = {};
     float m = -__builtin_inff(), l = 0.f;
-    const float sc = EX ? 1.f : a.scale * kLog2e;  // of scores as `raise` and `weigh` find them
-    const bool cap = EX && a.score.cap_log2 > 0.f, bias = EX && a.score.slopes;
-    float slope = bias ? a.score.slopes[head] * kLog2e : 0.f;
+    const float sc = RAW ? a.scale * kLog2e : 1.f;  // of scores as `raise` and `weigh` find them
+    const bool bias = EX && a.score.slopes;
+    float slope = bias ? a.score.slopes[head] * (RAW ? 1.f / a.scale : kLog2e) : 0.f;
     const int from = bias_from(my, s.len + tok) - 4 * hf;
 
     // ---- operand reads. Every lane offset is one opaque value, a single step from its array:
@@ -600,13 +631,58 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
 
     // ---- one tile: this wavefront's KB blocks of 32 keys
     f32x16 sv[KB];               // scores
+    // the bias of block kb's key r of a lane: -slope |from - j|. Keys of the cache that a row sees are
+    // not past `from` (either `from` is the row's own position or later, or it is its last key)
+    auto biased = [&](auto S, int kb, auto with) {
+        const int d = from - jpos[S.value] - 32 * (wk * KB + kb);
+        if (jpos[S.value] < s.len) {
+            const float b0 = -slope * static_cast<float>(d);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sv[kb][r] = with(fmaf(slope, static_cast<float>(8 * (r / 4) + r % 4), b0), r);
+        } else {
+            const float d0 = static_cast<float>(d);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sv[kb][r] = with(-slope * fabsf(d0 - static_cast<float>(8 * (r / 4) + r % 4)), r);
+        }
+    };
     auto scores = [&](auto S) {  // S^T = K Q^T
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             sv[kb] = f32x16{};
+            if (MODE == kRanged && RAW && bias)
+                biased(S, kb, [](float b, int) { return b; });
+        }
+        auto read = [&](int i) {
+            return *reinterpret_cast<const Frag *>(&KBUF(S)[koff[i % L::STEPS] + 32 * (i / L::STEPS) * ROWB]);
+        };
+        constexpr int N = KB * L::STEPS;
+        if constexpr (SCHED) {
+            // GS operands are read while the GS in front of them are multiplied. Left to itself the
+            // compiler kept one, and waited for LDS in front of every product
+            constexpr int GS = D == 128 ? 4 : 2;
+            Frag kf[2][GS];
 #pragma unroll
-            for (int st = 0; st < L::STEPS; ++st)
-                sv[kb] = L::qk(*reinterpret_cast<const Frag *>(&KBUF(S)[koff[st] + 32 * kb * ROWB]), q[st], sv[kb]);
+            for (int i = 0; i < GS; ++i)
+                kf[0][i] = read(i);
+#pragma unroll
+            for (int g = 0; g < N / GS; ++g) {
+#pragma unroll
+                for (int i = 0; i < GS && g + 1 < N / GS; ++i)
+                    kf[(g + 1) & 1][i] = read((g + 1) * GS + i);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < GS; ++i) {
+                    const int at = g * GS + i;
+                    sv[at / L::STEPS] = L::qk(kf[g & 1][i], q[at % L::STEPS], sv[at / L::STEPS]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                sv[i / L::STEPS] = L::qk(read(i), q[i % L::STEPS], sv[i / L::STEPS]);
         }
     };
     auto hide = [&](auto S) {  // scores of what the query does not attend to: -infinity
@@ -622,17 +698,26 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const uint32_t on = __builtin_amdgcn_sbfe(see, 8 * (r / 4) + r % 4, 1);  // all bits or none
-                sv[kb][r] = __uint_as_float((__float_as_uint(sv[kb][r]) & on) | (0xff800000u & ~on));
+                constexpr uint32_t hidden = POLY ? __builtin_bit_cast(uint32_t, kHidden) : 0xff800000u;
+                sv[kb][r] = __uint_as_float((__float_as_uint(sv[kb][r]) & on) | (hidden & ~on));
             }
         }
     };
+    Poly poly = {1.f, 0.f, 0.f, 0.f};
+    // scores as `weigh` takes them, where the products do not leave them so
     auto shape = [&](auto S) {
-        if (cap) {
+        if constexpr (MODE == kCapped) {
+            auto each = [&](auto f) {
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    sv[kb][r] = capped(sv[kb][r], a.score);
+                    for (int r = 0; r < 16; ++r)
+                        sv[kb][r] = f(sv[kb][r]);
+            };
+            if (a.score.fast)
+                each([&](float x) { return capped_any(x, a.score); });
+            else
+                each([&](float x) { return capped(x, a.score); });
         } else {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
@@ -640,12 +725,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         }
         if (bias) {
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                const float d0 = static_cast<float>(from - jpos[S.value] - 32 * (wk * KB + kb));
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    sv[kb][r] = fmaf(-slope, fabsf(d0 - static_cast<float>(8 * (r / 4) + r % 4)), sv[kb][r]);
-            }
+            for (int kb = 0; kb < KB; ++kb)
+                biased(S, kb, [&](float b, int r) { return sv[kb][r] + b; });
         }
     };
     // the query's new reference (a lane holds half of its keys; the other half's lane has the rest)
@@ -656,7 +737,11 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 mx = fmaxf(mx, sv[kb][r]);
-        mx = half_max(mx) * sc;
+        mx = half_max(mx);
+        if constexpr (POLY)
+            mx = mx == kHidden ? -__builtin_inff() : mx * poly(mx);
+        else
+            mx *= sc;
         if (__ballot(mx > m)) {
             const float mn = fmaxf(m, mx + kAbove);
             const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);  // equal infinities: 1
@@ -672,44 +757,92 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     auto weigh = [&](auto S) {
         constexpr int PARTS = 2 * KB;
         const float ref = m == -__builtin_inff() ? 0.f : m;
+        auto power = [&](float x) { return POLY ? fmaf(x, poly(x), -ref) : fmaf(x, sc, -ref); };
         float wt[PARTS][8];
         bf16x8 wb[PARTS];
+        auto make = [&](int x, int from, int to) {
 #pragma unroll
-        for (int x = 0; x <= PARTS; ++x) {
-            if (x < PARTS) {
+            for (int e = from; e < to; ++e)
+                wt[x][e] = __builtin_amdgcn_exp2f(power(sv[x / 2][8 * (x % 2) + e]));
+        };
+        auto add = [&](int x) {
+            if constexpr (EL == 2) {
+                // the sum is of the rounded weights, two per instruction
+                wb[x] = to_bf16x8(wt[x]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    l = add_pair(wb[x], e, l);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    wt[x][e] = __builtin_amdgcn_exp2f(fmaf(sv[x / 2][8 * (x % 2) + e], sc, -ref));
-                if constexpr (EL == 2) {
-                    // the sum is of the rounded weights, two per instruction
-                    wb[x] = to_bf16x8(wt[x]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        l = add_pair(wb[x], e, l);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        l += wt[x][e];
-                }
+                    l += wt[x][e];
             }
-            if (x > 0) {
-                const int row = 16 * (x - 1);
-                if constexpr (EL == 2) {
+        };
+        auto read = [&](int x, int d) {  // values of part x, channels of block d
+            return cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + 16 * x * ROWB])),
+                       tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (16 * x + 8) * ROWB])));
+        };
+        if constexpr (SCHED) {
+            // A part's values are read while weights are made. At headdim 128 two wavefronts share a
+            // SIMD: there they are read a part ahead, and a product is followed by a share of the next
+            // part's weights; at 64 the four of a SIMD cover each other, and registers are short.
+            constexpr int DB = D / 32;
+            constexpr bool AHEAD = D == 128;
+            bf16x8 vf[AHEAD ? 2 : 1][DB];
+            auto read_all = [&](int x) {
 #pragma unroll
-                    for (int d = 0; d < D / 32; ++d) {
-                        const bf16x8 vf = cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + row * ROWB])),
-                                              tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (row + 8) * ROWB])));
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, wb[x - 1], o[d], 0, 0, 0);
+                for (int d = 0; d < DB; ++d)
+                    vf[AHEAD ? x & 1 : 0][d] = read(x, d);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            auto multiply = [&](int x, int d) {
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[AHEAD ? x & 1 : 0][d], wb[x], o[d], 0, 0, 0);
+            };
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) {
+                if (AHEAD || x > 0)
+                    read_all(AHEAD ? x : x - 1);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    if (AHEAD && x > 0)
+                        multiply(x - 1, d);
+                    make(x, 8 * d / DB, 8 * (d + 1) / DB);
+                    if (AHEAD)
+                        __builtin_amdgcn_sched_barrier(0);
+                }
+                add(x);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int d = 0; d < DB && !AHEAD && x > 0; ++d)
+                    multiply(x - 1, d);
+            }
+            if (!AHEAD)
+                read_all(PARTS - 1);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                multiply(PARTS - 1, d);
+        } else {
+#pragma unroll
+            for (int x = 0; x <= PARTS; ++x) {
+                if (x < PARTS) {
+                    make(x, 0, 8);
+                    add(x);
+                }
+                if (x > 0) {
+                    if constexpr (EL == 2) {
+#pragma unroll
+                        for (int d = 0; d < D / 32; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(read(x - 1, d), wb[x - 1], o[d], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+#pragma unroll
+                            for (int d = 0; d < D / 32; ++d) {
+                                const int at = voff[0] + (16 * (x - 1) + 8 * (e / 4) + e % 4) * ROWB + 128 * d;
+                                o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(*reinterpret_cast<const float *>(&VBUF(S)[at]),
+                                                                            wt[x - 1][e], o[d], 0, 0, 0);
+                            }
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-#pragma unroll
-                        for (int d = 0; d < D / 32; ++d) {
-                            const int at = voff[0] + (row + 8 * (e / 4) + e % 4) * ROWB + 128 * d;
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(*reinterpret_cast<const float *>(&VBUF(S)[at]),
-                                                                        wt[x - 1][e], o[d], 0, 0, 0);
-                        }
                 }
             }
         }
@@ -761,10 +894,27 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             start(Int<1 - S.value>{});
         if (seen(S)) {
             scores(S);
-            if constexpr (EX)
-                shape(S);
-            if (!whole(S))
-                hide(S);
+            if constexpr (POLY) {
+                float top = 0.f;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        top = fmaxf(top, fabsf(sv[kb][r]));
+                // a NaN does not count as large: it goes through the polynomial as well
+                const bool all = whole(S), small = a.score.fast && !bias && all && __ballot(top > a.score.half_cap) == 0;
+                poly = small ? Poly{a.score.q[0], a.score.q[1], a.score.q[2], a.score.q[3]} : Poly{1.f, 0.f, 0.f, 0.f};
+                if (!small) {
+                    shape(S);
+                    if (!all)
+                        hide(S);
+                }
+            } else {
+                if constexpr (!RAW)
+                    shape(S);
+                if (!whole(S))
+                    hide(S);
+            }
             raise();
             weigh(S);
         }
@@ -792,7 +942,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             // nothing is kept in registers for it through the loop
             auto *args = (const AttnArgs *)__builtin_amdgcn_kernarg_segment_ptr();
             asm volatile("" : "+s"(args));
-            if (repair<T, D, EX>(*args, mine, odd[1], part, part_ml))
+            if (repair<T, D, MODE>(*args, mine, odd[1], part, part_ml))
                 return;
         }
     }
@@ -982,7 +1132,7 @@ auto by_rows(int64_t R, F f)
     }
 }
 
-template <bool EX>
+template <int MODE>
 struct Launch {
     const AttnArgs &a;
     const AttnPlan &p;
@@ -994,7 +1144,7 @@ struct Launch {
         using C = AttnCfg<T, D, WM, WK, TK>;
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
-        k_attn<T, D, WM, WK, TK, WPE, EX>
+        k_attn<T, D, WM, WK, TK, WPE, MODE>
             <<<dim3(static_cast<unsigned>(p.groups)), C::THREADS, 0, st>>>(a, p, part, ml);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.nsplit == 1)

@@ -1,5 +1,5 @@
 // Attention of a chunk over a paged cache: launch plans, and the launch of the kernels of
-// attn_kernel.h for plain scores (attn_scored.hip launches those for shaped and ranged ones).
+// attn_kernel.h for plain scores (attn_ranged.hip and attn_capped.hip launch the others).
 #include <algorithm>
 #include <cmath>
 
@@ -198,7 +198,7 @@ size_t attn_workspace(const AttnArgs &a, int D, bool bf16)
 
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st)
 {
-    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), Launch<false>{a, p, ws, st});
+    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), Launch<kPlain>{a, p, ws, st});
 }
 
 }  // namespace bdssm

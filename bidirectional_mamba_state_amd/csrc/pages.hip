@@ -113,6 +113,15 @@ __device__ __forceinline__ Span new_entries(const AdvanceArgs &a, int b)
                 static_cast<int>((end + page - 1) >> a.p.page_shift), len};
 }
 
+// What an entry that new tokens do not start is afterwards. The next query is at position len and
+// looks back to len - window + 1.
+__device__ __forceinline__ bool stays(const AdvanceArgs &a, const Span &s, int i, int e)
+{
+    const int64_t at = static_cast<int64_t>(i) << a.p.page_shift;
+    return i < s.from && is_page(a.p, e) &&
+           (a.window == 0 || at < a.sinks || at + (int64_t{1} << a.p.page_shift) > static_cast<int64_t>(s.len) - a.window + 1);
+}
+
 // empty entries among [from, to) of a row, by a workgroup
 __device__ __forceinline__ int empty_entries(const PoolArgs &a, const int *row, int from, int to, int *lds)
 {
@@ -176,7 +185,7 @@ __device__ __forceinline__ Span part_of(const PoolArgs &a, int part)
 __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
 {
     __shared__ int lds[4];
-    const int b = blockIdx.y, page = 1 << a.p.page_shift, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int b = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     if (b >= a.p.batch) {  // no streams
         if (threadIdx.x == 0)
             a.lacking[0] = 0;
@@ -190,10 +199,7 @@ __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
         if (i >= s.from && i < s.to)
             continue;
         const int e = in[i];
-        const int64_t at = static_cast<int64_t>(i) << a.p.page_shift;
-        // the next query is at position len and looks back to len - window + 1
-        const bool seen = a.window == 0 || at < a.sinks || at + page > static_cast<int64_t>(s.len) - a.window + 1;
-        const bool kept = i < s.from && seen && is_page(a.p, e);
+        const bool kept = stays(a, s, i, e);
         if (!kept && is_page(a.p, e))
             atomicSub(&a.p.uses_out[e], 1);
         if (in != out || !kept)
@@ -397,6 +403,267 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a)
     }
 }
 
+// ---- one workgroup
+// The same calls where the pool, the table and the streams are small: one launch instead of three,
+// since three cost more than the work (streams of 64 tokens: 11 us from the host in three, see the
+// limits at kSmallPages). Free pages and uses are held in LDS.
+constexpr int kSmallPages = 16384, kSmallRows = 1024, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+
+struct Small {
+    int list[kSmallPages];  // free pages in order; compact: where a page goes, from page n on
+    int uses[kSmallPages];
+    uint64_t bits[kSmallPages / 64];
+    int before[kSmallPages / 64];  // free pages in front of a word
+    int rows[3][kSmallRows];
+    int sums[kSmallWaves];
+};
+
+// Exclusive sums of v over the workgroup's threads; the whole sum in `all`.
+__device__ __forceinline__ int sums_before(int v, int *lds, int *all)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int n = v;
+#pragma unroll
+    for (int y = 1; y < 64; y *= 2) {
+        const int o = __shfl_up(n, y);
+        n += lane >= y ? o : 0;
+    }
+    __syncthreads();  // lds may still be read from an earlier sum
+    if (lane == 63)
+        lds[w] = n;
+    __syncthreads();
+    int front = 0, whole = 0;
+#pragma unroll
+    for (int x = 0; x < kSmallWaves; ++x) {
+        front += x < w ? lds[x] : 0;
+        whole += lds[x];
+    }
+    *all = whole;
+    return front + n - v;
+}
+
+// Uses and free bits into LDS, and the free pages in front of every word. Returns how many there are.
+__device__ __forceinline__ int small_snapshot(const PoolArgs &a, Small &m)
+{
+    const int lane = threadIdx.x & 63, words = (a.num_pages + 63) / 64;
+    int u[kSmallPages / kSmallThreads];
+#pragma unroll
+    for (int k = 0; k < kSmallPages / kSmallThreads; ++k) {
+        const int p = threadIdx.x + k * kSmallThreads;
+        u[k] = 1;
+        if (k * kSmallThreads < a.num_pages)
+            u[k] = a.uses[p < a.num_pages ? p : a.num_pages - 1];
+    }
+#pragma unroll
+    for (int k = 0; k < kSmallPages / kSmallThreads; ++k) {
+        const int p = threadIdx.x + k * kSmallThreads;
+        if (k * kSmallThreads >= a.num_pages)
+            break;
+        const uint64_t word = __ballot(p < a.num_pages && u[k] <= 0);
+        if (p < words * 64)
+            m.uses[p] = u[k] > 0 ? u[k] : 0;
+        if (lane == 0 && p < words * 64)
+            m.bits[p / 64] = word;
+    }
+    __syncthreads();
+    const int x = threadIdx.x;
+    int free;
+    const int n = sums_before(x < words ? __popcll(m.bits[x]) : 0, m.sums, &free);
+    if (x < words)
+        m.before[x] = n;
+    __syncthreads();
+    return free;
+}
+
+__device__ __forceinline__ int free_before(const Small &m, int p)
+{
+    return m.before[p / 64] + __popcll(m.bits[p / 64] & ((uint64_t{1} << (p & 63)) - 1));
+}
+
+// the first `most` free pages, in order
+__device__ __forceinline__ void small_list(const PoolArgs &a, Small &m, int most)
+{
+    for (int p = threadIdx.x; p < a.num_pages; p += kSmallThreads) {
+        if (!(m.bits[p / 64] >> (p & 63) & 1))
+            continue;
+        const int r = free_before(m, p);
+        if (r < most)
+            m.list[r] = p;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void small_uses_out(const PoolArgs &a, const Small &m)
+{
+    for (int p = threadIdx.x; p < a.num_pages; p += kSmallThreads)
+        a.uses_out[p] = m.uses[p];
+}
+
+// f(y, entry y of table[0 .. n)), or of both tables, for the entries of a thread; eight are loaded
+// before the first is used.
+template <typename F>
+__device__ __forceinline__ void small_entries(const int *table, int n, F f)
+{
+    constexpr int U = 8;
+    for (int y0 = threadIdx.x; y0 < n; y0 += U * kSmallThreads) {
+        int e[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int y = y0 + k * kSmallThreads;
+            e[k] = table[y < n ? y : n - 1];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (y0 + k * kSmallThreads < n)
+                f(y0 + k * kSmallThreads, e[k]);
+    }
+}
+
+__global__ __launch_bounds__(kSmallThreads) void k_advance_small(AdvanceArgs a, Divisor by_row)
+{
+    __shared__ Small m;
+    const int x = threadIdx.x, per = a.p.max_pages;
+    // a stream per thread: what its new tokens start, and how many of those entries are empty
+    Span s{};
+    int empty = 0;
+    if (x < a.p.batch) {
+        s = new_entries(a, x);
+        for (int i = s.from; i < s.to; ++i)
+            empty += !is_page(a.p, a.p.table[x * per + i]);
+        m.rows[0][x] = s.from, m.rows[1][x] = s.to, m.rows[2][x] = s.len;
+    }
+    const int free = small_snapshot(a.p, m);
+    int need;
+    int place = sums_before(empty, m.sums, &need);
+    small_list(a.p, m, need);
+    for (int i = s.from; i < s.to; ++i) {  // the stream's own thread; others have an empty span
+        const int e = a.p.table[x * per + i];
+        int to = e;
+        if (!is_page(a.p, e)) {
+            to = place < free ? m.list[place] : -1;
+            ++place;
+            if (to >= 0)
+                atomicAdd(&m.uses[to], 1);
+        }
+        if (to != e || a.p.table_out != a.p.table)
+            a.p.table_out[x * per + i] = to;
+    }
+    small_entries(a.p.table, a.p.batch * per, [&](int y, int e) {
+        const int b = by_row(y), i = y - b * per;
+        const Span r = {m.rows[0][b], m.rows[1][b], m.rows[2][b]};
+        if (i >= r.from && i < r.to)
+            return;
+        const bool kept = stays(a, r, i, e);
+        if (!kept && is_page(a.p, e))
+            atomicSub(&m.uses[e], 1);
+        if (a.p.table != a.p.table_out || !kept)
+            a.p.table_out[y] = kept ? e : -1;
+    });
+    __syncthreads();
+    small_uses_out(a.p, m);
+    if (x == 0)
+        a.lacking[0] = need > free ? need - free : 0;
+}
+
+__global__ __launch_bounds__(kSmallThreads) void k_fork_small(ForkArgs a, Divisor by_row)
+{
+    __shared__ Small m;
+    const int x = threadIdx.x, per = a.p.max_pages;
+    int *const first = m.rows[2];  // the first row with this parent
+    const int parent = x < a.p.batch ? a.parents[x] : -1;
+    const bool goes_on = parent >= 0 && parent < a.p.batch;
+    first[x] = INT_MAX;
+    __syncthreads();
+    if (goes_on)
+        atomicMin(&first[parent], x);
+    const int free = small_snapshot(a.p, m);
+    const int len = goes_on ? cached(a.p, parent) : 0, whole = len >> a.p.page_shift;
+    const bool again = goes_on && first[parent] != x;
+    int old = -1;
+    if (again && (len & ((1 << a.p.page_shift) - 1)))
+        old = a.p.table[parent * per + whole];
+    old = is_page(a.p, old) ? old : -1;
+    int need;
+    const int place = sums_before(old >= 0, m.sums, &need);
+    small_list(a.p, m, need);
+    const int fresh = old >= 0 && place < free ? m.list[place] : -1;
+    if (x < a.p.batch) {
+        a.lens_out[x] = len;
+        a.copies[2 * x] = fresh >= 0 ? old : -1;
+        a.copies[2 * x + 1] = fresh;
+        m.rows[0][x] = again ? whole : per;  // entries from here on are not the parent's
+        m.rows[1][x] = goes_on ? parent : -1;
+        m.rows[2][x] = fresh;  // every thread has read `first` before the list's last barrier
+    }
+    __syncthreads();
+    // the parents' entries, and what they replace; eight of a thread loaded before the first is used
+    constexpr int U = 8;
+    const int all = a.p.batch * per;
+    for (int y0 = x; y0 < all; y0 += U * kSmallThreads) {
+        int now[U], old[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int y = min(y0 + k * kSmallThreads, all - 1), b = by_row(y), p = m.rows[1][b];
+            old[k] = a.p.table[y];
+            now[k] = a.p.table[p < 0 ? y : p * per + y - b * per];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int y = y0 + k * kSmallThreads;
+            if (y >= all)
+                break;
+            const int b = by_row(y), i = y - b * per, from = m.rows[0][b], was = old[k];
+            int e = m.rows[1][b] >= 0 && i < from ? now[k] : -1;
+            if (i == from)
+                e = m.rows[2][b];
+            e = is_page(a.p, e) ? e : -1;
+            if (e != was) {
+                if (e >= 0)
+                    atomicAdd(&m.uses[e], 1);
+                if (is_page(a.p, was))
+                    atomicSub(&m.uses[was], 1);
+            }
+            a.p.table_out[y] = e;
+        }
+    }
+    __syncthreads();
+    small_uses_out(a.p, m);
+    if (x == 0)
+        a.lacking[0] = need > free ? need - free : 0;
+}
+
+__global__ __launch_bounds__(kSmallThreads) void k_compact_small(CompactArgs a)
+{
+    __shared__ Small m;
+    const int x = threadIdx.x, P = a.p.num_pages;
+    const int live = P - small_snapshot(a.p, m), moves = live < P ? free_before(m, live) : 0;
+    small_list(a.p, m, moves);
+    // where the pages from `live` on go: behind the list, which ends at moves <= live
+    for (int p = live + x; p < P; p += kSmallThreads) {
+        if (m.bits[p / 64] >> (p & 63) & 1)
+            m.list[p] = p;
+        else {
+            const int r = live - 1 - (p - free_before(m, p)), to = m.list[r];
+            m.list[p] = to;
+            m.uses[to] = m.uses[p];
+            m.uses[p] = 0;
+            a.copies[2 * r] = p, a.copies[2 * r + 1] = to;
+        }
+    }
+    for (int r = moves + x; r < P / 2; r += kSmallThreads)
+        a.copies[2 * r] = a.copies[2 * r + 1] = -1;
+    __syncthreads();
+    small_entries(a.p.table, a.p.batch * a.p.max_pages, [&](int y, int e) {
+        int to = is_page(a.p, e) ? e : -1;
+        to = to >= live ? m.list[to] : to;
+        if (to != e || a.p.table_out != a.p.table)
+            a.p.table_out[y] = to;
+    });
+    small_uses_out(a.p, m);
+    if (x == 0)
+        a.live[0] = live;
+}
+
 // ---- copies
 // A workgroup takes 16 KB of a page of one pool: entries along x, pools and parts along y. Threads
 // past the page's end read its last piece again, so that no load is conditional: a conditional one
@@ -440,6 +707,13 @@ bdssm_status check_pages_dims(const bdssm_pages_dims *d)
         static_cast<int64_t>(d->max_pages) * p > kMaxPosition)
         return BDSSM_ERR_UNSUPPORTED;
     return BDSSM_OK;
+}
+
+// Whether one workgroup takes a call. In LDS fit 16,384 pages and 1,024 streams; a table of up to
+// 65,536 entries is 64 turns of the workgroup.
+bool small(const bdssm_pages_dims *d)
+{
+    return d->num_pages <= kSmallPages && d->batch <= kSmallRows && static_cast<int64_t>(d->batch) * d->max_pages <= 65536;
 }
 
 int64_t chunks_of(const bdssm_pages_dims *d) { return (static_cast<int64_t>(d->num_pages) + kChunk - 1) / kChunk; }
@@ -552,6 +826,11 @@ extern "C" bdssm_status bdssm_pages_advance(const bdssm_pages_dims *dims, const 
         return BDSSM_ERR_SHAPE;
     a.starts = starts, a.block_len = block_len, a.window = window, a.sinks = sinks, a.lacking = lacking;
     hipStream_t st = static_cast<hipStream_t>(stream);
+    // a stream's new entries are one thread's there
+    if (small(dims) && block_len / dims->page_size <= 64) {
+        k_advance_small<<<1, kSmallThreads, 0, st>>>(a, Divisor(std::max(1, dims->max_pages)));
+        return launched(hipGetLastError());
+    }
     if (a.p.chunks + dims->batch > 0)
         k_advance_count<<<a.p.chunks + dims->batch, 256, 0, st>>>(a);
     if (a.p.chunks > 0)
@@ -574,6 +853,10 @@ extern "C" bdssm_status bdssm_pages_fork(const bdssm_pages_dims *dims, const bds
         return rc;
     a.parents = parents, a.lens_out = lens_out, a.copies = copies, a.lacking = lacking;
     hipStream_t st = static_cast<hipStream_t>(stream);
+    if (small(dims)) {
+        k_fork_small<<<1, kSmallThreads, 0, st>>>(a, Divisor(std::max(1, dims->max_pages)));
+        return launched(hipGetLastError());
+    }
     const int rows = (dims->batch + 3) / 4;
     if (a.p.chunks + rows > 0)
         k_fork_count<<<a.p.chunks + rows, 256, 0, st>>>(a);
@@ -598,6 +881,10 @@ extern "C" bdssm_status bdssm_pages_compact(const bdssm_pages_dims *dims, const 
         return rc;
     a.copies = copies, a.live = live;
     hipStream_t st = static_cast<hipStream_t>(stream);
+    if (small(dims)) {
+        k_compact_small<<<1, kSmallThreads, 0, st>>>(a);
+        return launched(hipGetLastError());
+    }
     if (a.p.chunks > 0)
         k_snapshot<<<a.p.chunks, 256, 0, st>>>(a.p);
     k_compact_list<<<std::max(1, a.p.chunks), 256, 0, st>>>(a);

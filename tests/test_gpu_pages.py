@@ -154,7 +154,9 @@ def random_cache(g, batch, per, P, page, gaps=0.1, share=0.2):
 
 
 SHAPES = [(1, 1, 1, 16), (1, 5, 7, 16), (3, 9, 40, 32), (7, 33, 200, 16), (2, 300, 700, 256), (64, 40, 2000, 64),
-          (5, 3000, 9000, 16), (300, 3, 4097, 128), (3, 4, 4096, 16), (9, 0, 5, 16)]
+          (5, 3000, 9000, 16), (300, 3, 4097, 128), (3, 4, 4096, 16), (9, 0, 5, 16), (1024, 16, 16384, 16),
+          # more pages, entries or streams than one workgroup takes
+          (3, 400, 16385, 16), (4, 16400, 12000, 16), (1025, 4, 4500, 32), (2, 6000, 70000, 64)]
 
 
 @pytest.mark.parametrize("in_place", [False, True])
@@ -170,6 +172,18 @@ def test_advance(shape, in_place):
         counts = [int(g.integers(0, 5 * page))] * batch if even else [int(x) for x in g.integers(0, 5 * page, batch)]
         d = Device(m)
         same(d.advance(counts, window, sinks, in_place, even), m.advance(counts, window, sinks), f"trial {trial}")
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_advance_by_many_pages(in_place):
+    """A prompt's pages at once: hundreds of new entries of a stream, some of them held already."""
+    _case("many new pages")
+    g = np.random.default_rng(2)
+    m = random_cache(g, 3, 900, 4000, 16)
+    m.lens[:] = [0, 100, 5000]
+    same(Device(m).advance([14000, 1040, 5000], 0, 0, in_place), m.advance([14000, 1040, 5000]), "many")
+    m = random_cache(g, 2, 90, 400, 16)
+    same(Device(m).advance([64 * 16 + 15, 3], 0, 0, in_place), m.advance([64 * 16 + 15, 3]), "at the limit")
 
 
 @pytest.mark.parametrize("in_place", [False, True])
