@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libbdssm.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "scan_valu.hip", "block_step_mfma.hip", "block_step_lat.hip", "block_step_bw.hip",
            "prefix_mfma.hip", "graph.hip", "conv.hip", "norm.hip", "attn.hip",
-           "attn_mfma.hip", "attn_ranged.hip", "attn_capped.hip",
+           "attn_mfma.hip", "attn_ranged.hip", "attn_capped.hip", "attn_exact.hip",
            "rotary.hip", "pages.hip"]
 ARCH = "gfx950"
 

@@ -42,7 +42,7 @@ struct AttnScoring {
     float two_x_log2 = 0.f;           // 2 x_per_score log2 e
     float half_cap = 0.f;             // the score (before scale) that is half of the cap
     float q[4] = {};                  // polynomial of small scores, see attn_kernel.h
-    int fast = 0;                     // by the tile: bf16, a cap of 256 or less
+    bool fast = false;                // bf16, a cap of 256 or less
     const float *slopes = nullptr;    // [H]
     const int *prefix = nullptr;      // [batch]
     const int *first = nullptr, *last = nullptr;  // [tokens]
@@ -132,5 +132,6 @@ size_t attn_workspace(const AttnArgs &a, int D, bool bf16);
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 hipError_t launch_attn_ranged(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 hipError_t launch_attn_capped(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
+hipError_t launch_attn_exact(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 
 }  // namespace bdssm

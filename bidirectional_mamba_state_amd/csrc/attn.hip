@@ -215,7 +215,9 @@ bdssm_status attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chun
         if (overlap(rw, ro))
             return BDSSM_ERR_ALIAS;
     }
-    const auto launch = !scored ? launch_attn : a.score.cap_log2 > 0.f ? launch_attn_capped : launch_attn_ranged;
+    const auto launch = !scored ? launch_attn : a.score.cap_log2 == 0.f ? launch_attn_ranged
+                        : a.score.fast          ? launch_attn_capped
+                                                : launch_attn_exact;
     return launched(launch(a, dims->headdim, bf16, p, workspace, static_cast<hipStream_t>(stream)));
 }
 

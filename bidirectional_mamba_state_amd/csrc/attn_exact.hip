@@ -1,0 +1,12 @@
+// Attention of a chunk over a paged cache with scores capped as exactly as float32 can, and ranges and a bias
+// (bdssm_attn_step_ex): the kernels of attn_kernel.h, a unit to each of their modes.
+#include "attn_kernel.h"
+
+namespace bdssm {
+
+hipError_t launch_attn_exact(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st)
+{
+    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), Launch<kExact>{a, p, ws, st});
+}
+
+}  // namespace bdssm

@@ -198,8 +198,9 @@ __device__ __forceinline__ int prefix_of(const AttnArgs &a, int b, int end)
 }
 
 // What a kernel does to scores and ranges beyond the mask of bdssm_attn_step: nothing; ranges of rows and
-// a bias, each where it is given (AttnArgs::score); a cap, and those.
-enum Mode { kPlain, kRanged, kCapped };
+// a bias, each where it is given (AttnArgs::score); a cap, and those: as exactly as bf16 weights ask for
+// (a cap of 256 or less, AttnScoring::fast), or as float32 can.
+enum Mode { kPlain, kRanged, kCapped, kExact };
 
 // Shaped scores, in powers of two.
 //
@@ -207,21 +208,40 @@ enum Mode { kPlain, kRanged, kCapped };
 // some |x|; and 1 - 2 / (1 + e^2x), whose error is a few 2^-24 of c, and which an infinite score takes
 // to +-1. Each costs: the polynomial a multiplication and an addition a term, the other two
 // transcendentals, which take as long as eight additions.
-//  - Exactly (float32, or a cap above 256): six terms up to 0.6 (2.5e-9), the other form from there on,
-//    where it is a few 2^-24 of the score too.
-//  - For bf16 (see AttnScoring::fast): by the tile. Where a wavefront sees a whole tile and all of its
-//    scores are below c / 2, four terms (5.4e-7 of the score: up to 1e-4 of a power of two, a fortieth
-//    of the rounding of a bf16 weight), made along with the weights, where the products hide them; else
-//    the other form for all (a few 2^-24 of c).
+//  - kExact: six terms up to 0.6 (2.5e-9), the other form from there on, where it is a few 2^-24 of the
+//    score too; of both, where a wavefront's scores of a tile are not all small, the one that applies.
+//  - kCapped: the other form (a few 2^-24 of c). At headdim 128, where a wavefront sees a whole tile and
+//    all of its scores are below c / 2, four terms instead (5.4e-7 of the score: up to 1e-4 of a power
+//    of two, a fortieth of the rounding of a bf16 weight), made along with the weights, where the
+//    products hide them (a prompt of 8,192 on 8,192: 1.30 ms, 1.48 in the other form, 2.0 in front of
+//    the weights). At 64 a wavefront has no registers for both ways: what is saved goes into spills.
+//
+// Constants are operands of the instructions themselves (add_mul): as values each took a vector
+// register through the loop over tiles.
+template <uint32_t BITS>
+__device__ __forceinline__ float add_mul(float a, float b)  // a b + constant
+{
+    float r;
+    asm("v_fmaak_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "n"(BITS));
+    return r;
+}
+__device__ __forceinline__ float tanh_near(float x, float u)  // u = x^2, up to 0.36
+{
+    constexpr auto bits = [](float c) { return __builtin_bit_cast(uint32_t, c); };
+    float t = u * -0.00585216868f + 0.020753629f;
+    t = add_mul<bits(-0.0537687048f)>(t, u);
+    t = add_mul<bits(0.13331689f)>(t, u);
+    t = add_mul<bits(-0.333332833f)>(t, u);
+    return fmaf(t * u, x, x);
+}
+__device__ __forceinline__ float capped_near(float s, const AttnScoring &g)
+{
+    const float x = s * g.x_per_score;
+    return g.cap_log2 * tanh_near(x, x * x);
+}
 __device__ __forceinline__ float capped(float s, const AttnScoring &g)
 {
-    const float x = s * g.x_per_score, u = x * x;
-    float t = -0.00585216868f;
-    t = fmaf(t, u, 0.020753629f);
-    t = fmaf(t, u, -0.0537687048f);
-    t = fmaf(t, u, 0.13331689f);
-    t = fmaf(t, u, -0.333332833f);
-    t = fmaf(t * u, x, x);
+    const float x = s * g.x_per_score, u = x * x, t = tanh_near(x, u);
     float far = fmaf(-2.f, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * (2.f * kLog2e))), 1.f);
     asm("" : "+v"(far));  // both, then one of the two: no branch around each score
     return g.cap_log2 * (u < 0.36f ? t : far);
@@ -232,7 +252,7 @@ __device__ __forceinline__ float capped_any(float s, const AttnScoring &g)
     const float r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s * g.two_x_log2));
     return fmaf(r, -2.f * g.cap_log2, g.cap_log2);
 }
-// The polynomial of a tile: that of small scores, or 1 where the scores are shaped already.
+// small scores: s times this
 struct Poly {
     float q0, q1, q2, q3;
     __device__ __forceinline__ float operator()(float s) const
@@ -241,8 +261,6 @@ struct Poly {
         return fmaf(u, fmaf(u, fmaf(u, q3, q2), q1), q0);
     }
 };
-// A score that is not attended to where Poly makes the weights: its square is finite, its power of two 0.
-constexpr float kHidden = -0x1p60f;
 
 // Bias: a slope times the distance to the key. The softmax does not change when a row's scores
 // move together, so the distance is taken from the nearest position that the row attends to
@@ -331,7 +349,7 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional
                     for (int c = 0; c < D; ++c)
                         sj = fmaf(static_cast<float>(q[c]), static_cast<float>(k[c]), sj);
                 if constexpr (EX) {
-                    sj = MODE == kCapped ? capped(sj, a.score) : sj * (a.scale * kLog2e);
+                    sj = MODE >= kCapped ? capped(sj, a.score) : sj * (a.scale * kLog2e);
                     if (a.score.slopes)
                         sj = fmaf(-slope, fabsf(static_cast<float>(bias_from(see, s.len + tok) - j)), sj);
                 }
@@ -398,8 +416,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     // Whether `raise` and `weigh` find raw scores, to be scaled: a bias is then what the products start
     // from. float32 adds it up in up to 64 products, each with its rounding, so there it comes after.
     constexpr bool RAW = MODE == kPlain || (MODE == kRanged && EL == 2);
-    constexpr bool POLY = MODE == kCapped && EL == 2;  // weights are made by a tile's polynomial
-    constexpr bool SCHED = MODE != kPlain && EL == 2;  // the order of LDS reads and products is given
+    constexpr bool POLY = MODE == kCapped && D == 128;  // weights may be made by the cap's polynomial
+    constexpr bool SCHED = MODE != kPlain;  // the order of LDS reads and products is given
     constexpr uint64_t kAll = TK < 64 ? 0xffffffffull : ~0ull;  // a mask of keys with all of them
     static_assert(C::TILE_BYTES % (1024 * NW) == 0 && TK % (32 * WK) == 0, "tile shape");
 
@@ -636,15 +654,29 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     auto biased = [&](auto S, int kb, auto with) {
         const int d = from - jpos[S.value] - 32 * (wk * KB + kb);
         if (jpos[S.value] < s.len) {
-            const float b0 = -slope * static_cast<float>(d);
+            // key r is 8 (r / 4) + r % 4 further on. In steps of 1, 2 and 4 slopes, which instructions
+            // hold themselves; other factors would take a register each
+            float b = -slope * static_cast<float>(d);
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                sv[kb][r] = with(fmaf(slope, static_cast<float>(8 * (r / 4) + r % 4), b0), r);
+            for (int r = 0; r < 16; r += 4) {
+                const float b1 = b + slope;
+                sv[kb][r] = with(b, r);
+                sv[kb][r + 1] = with(b1, r + 1);
+                sv[kb][r + 2] = with(fmaf(slope, 2.f, b), r + 2);
+                sv[kb][r + 3] = with(fmaf(slope, 2.f, b1), r + 3);
+                b = fmaf(slope, 4.f, fmaf(slope, 4.f, b));
+            }
         } else {
-            const float d0 = static_cast<float>(d);
+            float far = static_cast<float>(d);
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                sv[kb][r] = with(-slope * fabsf(d0 - static_cast<float>(8 * (r / 4) + r % 4)), r);
+            for (int r = 0; r < 16; r += 4) {
+                const float far1 = far - 1.f;
+                sv[kb][r] = with(-slope * fabsf(far), r);
+                sv[kb][r + 1] = with(-slope * fabsf(far1), r + 1);
+                sv[kb][r + 2] = with(-slope * fabsf(far - 2.f), r + 2);
+                sv[kb][r + 3] = with(-slope * fabsf(far1 - 2.f), r + 3);
+                far = far - 4.f - 4.f;
+            }
         }
     };
     auto scores = [&](auto S) {  // S^T = K Q^T
@@ -661,7 +693,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         if constexpr (SCHED) {
             // GS operands are read while the GS in front of them are multiplied. Left to itself the
             // compiler kept one, and waited for LDS in front of every product
-            constexpr int GS = D == 128 ? 4 : 2;
+            constexpr int GS = EL == 2 && D == 128 ? 4 : 2;
             Frag kf[2][GS];
 #pragma unroll
             for (int i = 0; i < GS; ++i)
@@ -698,15 +730,23 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const uint32_t on = __builtin_amdgcn_sbfe(see, 8 * (r / 4) + r % 4, 1);  // all bits or none
-                constexpr uint32_t hidden = POLY ? __builtin_bit_cast(uint32_t, kHidden) : 0xff800000u;
-                sv[kb][r] = __uint_as_float((__float_as_uint(sv[kb][r]) & on) | (hidden & ~on));
+                sv[kb][r] = __uint_as_float((__float_as_uint(sv[kb][r]) & on) | (0xff800000u & ~on));
             }
         }
     };
-    Poly poly = {1.f, 0.f, 0.f, 0.f};
+    const Poly poly = {a.score.q[0], a.score.q[1], a.score.q[2], a.score.q[3]};
+    auto largest = [&]() {  // magnitude of a lane's scores; a NaN does not count
+        float top = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                top = fmaxf(top, fabsf(sv[kb][r]));
+        return top;
+    };
     // scores as `weigh` takes them, where the products do not leave them so
     auto shape = [&](auto S) {
-        if constexpr (MODE == kCapped) {
+        if constexpr (MODE >= kCapped) {
             auto each = [&](auto f) {
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -714,8 +754,10 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
                     for (int r = 0; r < 16; ++r)
                         sv[kb][r] = f(sv[kb][r]);
             };
-            if (a.score.fast)
+            if constexpr (MODE == kCapped)
                 each([&](float x) { return capped_any(x, a.score); });
+            else if (EL == 4 && __ballot(largest() * a.score.x_per_score > 0.6f) == 0)
+                each([&](float x) { return capped_near(x, a.score); });
             else
                 each([&](float x) { return capped(x, a.score); });
         } else {
@@ -729,8 +771,9 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
                 biased(S, kb, [&](float b, int r) { return sv[kb][r] + b; });
         }
     };
-    // the query's new reference (a lane holds half of its keys; the other half's lane has the rest)
-    auto raise = [&]() {
+    // Form 1: the weights take raw scores through the tile's polynomial; 0: scores times sc.
+    // The query's new reference (a lane holds half of its keys; the other half's lane has the rest)
+    auto raise = [&](auto form) {
         float mx = sv[0][0];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -738,8 +781,8 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             for (int r = 0; r < 16; ++r)
                 mx = fmaxf(mx, sv[kb][r]);
         mx = half_max(mx);
-        if constexpr (POLY)
-            mx = mx == kHidden ? -__builtin_inff() : mx * poly(mx);
+        if constexpr (form.value == 1)
+            mx *= poly(mx);
         else
             mx *= sc;
         if (__ballot(mx > m)) {
@@ -754,10 +797,10 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     };
     // weights, and O^T += V^T P^T one part of 16 keys behind them, so that a wavefront's products
     // and exponentials overlap
-    auto weigh = [&](auto S) {
+    auto weigh = [&](auto S, auto form) {
         constexpr int PARTS = 2 * KB;
         const float ref = m == -__builtin_inff() ? 0.f : m;
-        auto power = [&](float x) { return POLY ? fmaf(x, poly(x), -ref) : fmaf(x, sc, -ref); };
+        auto power = [&](float x) { return form.value == 1 ? fmaf(x, poly(x), -ref) : fmaf(x, sc, -ref); };
         float wt[PARTS][8];
         bf16x8 wb[PARTS];
         auto make = [&](int x, int from, int to) {
@@ -779,10 +822,43 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
             }
         };
         auto read = [&](int x, int d) {  // values of part x, channels of block d
-            return cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + 16 * x * ROWB])),
-                       tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[voff[d] + (16 * x + 8) * ROWB])));
+            const int at = voff[d] + 16 * x * ROWB;
+            return cat(tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[at])),
+                       tr_read(reinterpret_cast<const __bf16 *>(&VBUF(S)[at + 8 * ROWB])));
         };
-        if constexpr (SCHED) {
+        if constexpr (SCHED && EL == 4) {
+            // values of four keys are read while the four in front of them are multiplied, the next
+            // part's weights made between the products
+            constexpr int DB = D / 32;
+            float vf[2][4][DB];
+            auto read_four = [&](int g) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        vf[g & 1][e][d] = *reinterpret_cast<const float *>(&VBUF(S)[voff[0] + (8 * g + e) * ROWB + 128 * d]);
+            };
+            read_four(0);
+            make(0, 0, 8);
+            add(0);
+#pragma unroll
+            for (int g = 0; g < 2 * PARTS; ++g) {
+                if (g + 1 < 2 * PARTS)
+                    read_four(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf[g & 1][e][d], wt[g / 2][4 * (g & 1) + e], o[d], 0, 0, 0);
+                    if (g / 2 + 1 < PARTS)
+                        make(g / 2 + 1, 4 * (g & 1) + e, 4 * (g & 1) + e + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (g % 2 == 1 && g / 2 + 1 < PARTS)
+                    add(g / 2 + 1);
+            }
+        } else if constexpr (SCHED) {
             // A part's values are read while weights are made. At headdim 128 two wavefronts share a
             // SIMD: there they are read a part ahead, and a product is followed by a share of the next
             // part's weights; at 64 the four of a SIMD cover each other, and registers are short.
@@ -895,28 +971,23 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
         if (seen(S)) {
             scores(S);
             if constexpr (POLY) {
-                float top = 0.f;
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        top = fmaxf(top, fabsf(sv[kb][r]));
-                // a NaN does not count as large: it goes through the polynomial as well
-                const bool all = whole(S), small = a.score.fast && !bias && all && __ballot(top > a.score.half_cap) == 0;
-                poly = small ? Poly{a.score.q[0], a.score.q[1], a.score.q[2], a.score.q[3]} : Poly{1.f, 0.f, 0.f, 0.f};
-                if (!small) {
-                    shape(S);
-                    if (!all)
-                        hide(S);
+                const bool all = whole(S), small = !bias && all && __ballot(largest() > a.score.half_cap) == 0;
+                if (small) {
+                    raise(Int<1>{});
+                    weigh(S, Int<1>{});
+                    return;
                 }
+                shape(S);
+                if (!all)
+                    hide(S);
             } else {
                 if constexpr (!RAW)
                     shape(S);
                 if (!whole(S))
                     hide(S);
             }
-            raise();
-            weigh(S);
+            raise(Int<0>{});
+            weigh(S, Int<0>{});
         }
     };
     if (t0 < t1)
@@ -1141,6 +1212,9 @@ struct Launch {
     template <typename T, int D, int WM, int WK, int TK, int WPE>
     hipError_t operator()() const
     {
+        if constexpr (MODE == kCapped && sizeof(T) == 4) {
+            return hipErrorInvalidValue;  // float32 is exact
+        } else {
         using C = AttnCfg<T, D, WM, WK, TK>;
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
@@ -1154,6 +1228,7 @@ struct Launch {
         else
             join<T, D, 8>(a, p.nsplit, part, ml, st);
         return hipGetLastError();
+        }
     }
 };
 

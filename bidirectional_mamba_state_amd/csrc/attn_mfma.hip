@@ -1,5 +1,5 @@
 // Attention of a chunk over a paged cache: launch plans, and the launch of the kernels of
-// attn_kernel.h for plain scores (attn_ranged.hip and attn_capped.hip launch the others).
+// attn_kernel.h for plain scores (attn_ranged.hip, attn_capped.hip and attn_exact.hip launch the others).
 #include <algorithm>
 #include <cmath>
 
