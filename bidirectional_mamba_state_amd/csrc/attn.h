@@ -46,6 +46,7 @@ struct AttnScoring {
     const float *slopes = nullptr;    // [H]
     const int *prefix = nullptr;      // [batch]
     const int *first = nullptr, *last = nullptr;  // [tokens]
+    bool ranged() const { return first || last; }
 };
 
 struct AttnArgs {
@@ -121,7 +122,9 @@ struct AttnPlan {
     int rt_fast;
     Divisor by_inner, by_units, by_kv, by_split;  // nrt_sub or per_xcd, units / sub, KV, nsplit
     int64_t groups;                    // workgroups; more than kMaxGroups cannot be launched
-    size_t ml_bytes, ws_bytes;         // workspace: maxima and sums first, then rows (0 unless split)
+    size_t ml_bytes, ws_bytes;         // workspace: maxima and sums first, then rows (0 unless split),
+    size_t order_bytes;                // at its end the order of row tiles (0: as they come)
+    int order_shift;                   // key tiles of a row tile, in powers of two, that count as alike
 };
 
 AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);

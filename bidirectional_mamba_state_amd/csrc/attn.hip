@@ -170,6 +170,22 @@ bdssm_status prepare_scores(const bdssm_attn_scores *s, float scale, bool bf16, 
     return BDSSM_OK;
 }
 
+// Workspace of a step whose scoring is a.score.
+size_t step_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len, const bdssm_attn_mask *mask, AttnArgs a)
+{
+    if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK || block_len < 0 || max_len < 0 ||
+        static_cast<int64_t>(max_len) + block_len > kMaxPosition)
+        return SIZE_MAX;
+    if (dims->batch == 0 || block_len == 0)
+        return 0;
+    a.batch = dims->batch, a.H = dims->nheads, a.KV = dims->kv_heads;
+    a.block_len = block_len, a.max_len = max_len;
+    a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
+    if (!rows_fit(a))
+        return SIZE_MAX;
+    return attn_workspace(a, dims->headdim, dims->dtype == BDSSM_BF16);
+}
+
 bdssm_status attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_kv_cache *cache,
                        const bdssm_attn_mask *mask, const bdssm_attn_scores *scores, bool scored, void *out, void *workspace,
                        size_t workspace_bytes, void *stream)
@@ -229,18 +245,7 @@ using namespace bdssm;
 extern "C" size_t bdssm_attn_step_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len,
                                             const bdssm_attn_mask *mask)
 {
-    if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK || block_len < 0 || max_len < 0 ||
-        static_cast<int64_t>(max_len) + block_len > kMaxPosition)
-        return SIZE_MAX;
-    if (dims->batch == 0 || block_len == 0)
-        return 0;
-    AttnArgs a{};
-    a.batch = dims->batch, a.H = dims->nheads, a.KV = dims->kv_heads;
-    a.block_len = block_len, a.max_len = max_len;
-    a.block = mask->block, a.window = mask->window, a.sinks = mask->sinks;
-    if (!rows_fit(a))
-        return SIZE_MAX;
-    return attn_workspace(a, dims->headdim, dims->dtype == BDSSM_BF16);
+    return step_workspace(dims, block_len, max_len, mask, AttnArgs{});
 }
 
 extern "C" size_t bdssm_attn_step_ex_workspace(const bdssm_attn_dims *dims, int32_t block_len, int32_t max_len,
@@ -251,7 +256,7 @@ extern "C" size_t bdssm_attn_step_ex_workspace(const bdssm_attn_dims *dims, int3
     if (check_attn_dims(dims) != BDSSM_OK || check_attn_mask(mask) != BDSSM_OK ||
         prepare_scores(scores, mask->scale, dims->dtype == BDSSM_BF16, &a, r) != BDSSM_OK)
         return SIZE_MAX;
-    return bdssm_attn_step_workspace(dims, block_len, max_len, mask);
+    return step_workspace(dims, block_len, max_len, mask, a);
 }
 
 extern "C" bdssm_status bdssm_attn_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk,

@@ -393,6 +393,53 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional
     return true;
 }
 
+// The row tiles of a stream whose rows have ranges, the longest first: what a tile has to walk is in
+// device memory, and workgroups that take more than one round end together only so (documents of 350
+// to 1,050 tokens in a prompt: without it some CUs had twice the average). A tile counts as the keys
+// from its first row's lower to its last row's upper bound; 1,024 classes of them are sorted by
+// counting, in no order inside a class (row tiles do not depend on one another).
+__global__ __launch_bounds__(1024) void k_attn_order(AttnArgs a, int nrt, int rows, int tk, int shift, int *order)
+{
+    __shared__ int at[1024], sums[16];
+    const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const AttnStream s = attn_stream(a, b);
+    const int end = s.len + (a.k ? s.n : 0), prefix = prefix_of(a, b, end), G = static_cast<int>(a.by_group.d);
+    const int64_t all = static_cast<int64_t>(s.n) * G;
+    auto kind = [&](int rt) {  // 0: the longest
+        const int64_t r0 = static_cast<int64_t>(rt) * rows, r1 = r0 + rows < all ? r0 + rows : all;
+        int keys = 0;
+        if (r0 < r1) {
+            const Sight x = sight_of<true>(a, s, end, prefix, a.by_group(static_cast<int>(r0)));
+            const Sight y = sight_of<true>(a, s, end, prefix, a.by_group(static_cast<int>(r1 - 1)));
+            const int lo = x.lo < y.lo ? x.lo : y.lo, hi = x.hi > y.hi ? x.hi : y.hi;
+            keys = lo < hi ? hi - lo : 0;
+        }
+        const int tiles = (keys / tk + (keys > 0)) >> shift;
+        return 1023 - (tiles < 1023 ? tiles : 1023);
+    };
+    at[threadIdx.x] = 0;
+    __syncthreads();
+    for (int rt = threadIdx.x; rt < nrt; rt += 1024)
+        atomicAdd(&at[kind(rt)], 1);
+    __syncthreads();
+    const int mine = at[threadIdx.x];
+    int n = mine;
+#pragma unroll
+    for (int y = 1; y < 64; y *= 2) {
+        const int o = __shfl_up(n, y);
+        n += lane >= y ? o : 0;
+    }
+    if (lane == 63)
+        sums[w] = n;
+    __syncthreads();
+    for (int x = 0; x < w; ++x)
+        n += sums[x];
+    at[threadIdx.x] = n - mine;
+    __syncthreads();
+    for (int rt = threadIdx.x; rt < nrt; rt += 1024)
+        order[static_cast<int64_t>(b) * nrt + atomicAdd(&at[kind(rt)], 1)] = rt;
+}
+
 template <typename T, int D, int WM, int WK, int TK>
 struct AttnCfg {
     static constexpr int NW = WM * WK, THREADS = 64 * NW, RT = 32 * WM;
@@ -401,7 +448,8 @@ struct AttnCfg {
 
 template <typename T, int D, int WM, int WK, int TK, int WPE, int MODE>
 __global__ __launch_bounds__((AttnCfg<T, D, WM, WK, TK>::THREADS))
-__attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan pl, float *part, float2 *part_ml)
+__attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan pl, float *part, float2 *part_ml,
+                                                                      const int *order)
 {
     using C = AttnCfg<T, D, WM, WK, TK>;
     using L = Tile<T, D>;
@@ -442,8 +490,10 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const int rt_up = (pl.rt_fast ? inner : outer) * pl.sub + which;
     if (rt_up >= pl.nrt)
         return;
-    const int rt = a.block ? pl.nrt - 1 - rt_up : rt_up;  // ordered: the longest ranges first
     const int uk = pl.by_kv(u), kvh = pl.by_kv.rest(u), b = pl.by_split(uk), split = pl.by_split.rest(uk);
+    int rt = a.block ? pl.nrt - 1 - rt_up : rt_up;  // ordered: the longest ranges first
+    if (EX && order)
+        rt = __builtin_amdgcn_readfirstlane(order[static_cast<int64_t>(b) * pl.nrt + rt_up]);
     const int G = static_cast<int>(a.by_group.d);
     const int *table = a.table + static_cast<int64_t>(b) * a.max_pages;
     auto page_no = [&](int i) { return a.max_pages > 0 ? table[i < a.max_pages ? i : a.max_pages - 1] : -1; };
@@ -1181,16 +1231,20 @@ void join(const AttnArgs &a, int nsplit, const float *part, const float2 *ml, hi
 //  bf16   up to 64 rows: 2 x 2 (16 rows a head group, 8 streams of 32,768, headdim 128: 107 us,
 //         115 us as 8 x 1); more: 8 x 1 (128 rows, headdim 64: 62 us, 77 us as 2 x 2). Up to 32 rows
 //         as 1 x 4 with tiles of 128 is no faster: 6 rows on 255 keys 8.4 us, 8.9 so, on 1,000 keys
-//         of headdim 128 12.1, 15.6 so, on 16,384 keys the same
+//         of headdim 128 12.1, 15.6 so, on 16,384 keys the same. More, where rows have ranges of
+//         their own: 4 x 1, which waste less at a document's borders (8,191 tokens of 16 heads over 4
+//         in documents of 700, headdim 128: 72 us, 81 as 8 x 1; in one: 205 and 230)
 //  f32    up to 32 rows of headdim 64: 1 x 4 (32 rows, 8 streams of 4,096: 28 us, 32 us as 2 x 2,
 //         47 us as 4 x 1); up to 64 rows: 2 x 2 (64 rows: 34 us, 49 us as 4 x 1; headdim 128:
 //         58 us, 83 us); more: 4 x 1, whose products leave no room for more wavefronts
 template <typename T, int D, typename F>
-auto by_rows(int64_t R, F f)
+auto by_rows(int64_t R, bool ranged, F f)
 {
     if constexpr (sizeof(T) == 2) {
         if (R <= 64)
             return f.template operator()<T, D, 2, 2, 64, (D == 64 ? 3 : 2)>();
+        if (ranged)
+            return f.template operator()<T, D, 4, 1, 64, (D == 64 ? 3 : 2)>();
         return f.template operator()<T, D, 8, 1, 64, (D == 64 ? 4 : 2)>();
     } else {
         if constexpr (D == 64) {
@@ -1212,14 +1266,28 @@ struct Launch {
     template <typename T, int D, int WM, int WK, int TK, int WPE>
     hipError_t operator()() const
     {
-        if constexpr (MODE == kCapped && sizeof(T) == 4) {
-            return hipErrorInvalidValue;  // float32 is exact
-        } else {
+        // not built: float32 is exact, and plain rows have no ranges
+        constexpr bool never = (MODE == kCapped && sizeof(T) == 4) || (MODE == kPlain && sizeof(T) == 2 && WM == 4);
+        if constexpr (never)
+            return hipErrorInvalidValue;
+        else
+            return launch<T, D, WM, WK, TK, WPE>();
+    }
+    template <typename T, int D, int WM, int WK, int TK, int WPE>
+    hipError_t launch() const
+    {
         using C = AttnCfg<T, D, WM, WK, TK>;
         float2 *ml = static_cast<float2 *>(ws);
         float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.ml_bytes);
+        int *order = nullptr;
+        if constexpr (MODE != kPlain) {
+            if (p.order_bytes > 0) {
+                order = reinterpret_cast<int *>(static_cast<char *>(ws) + p.ws_bytes - p.order_bytes);
+                k_attn_order<<<a.batch, 1024, 0, st>>>(a, p.nrt, C::RT, TK, p.order_shift, order);
+            }
+        }
         k_attn<T, D, WM, WK, TK, WPE, MODE>
-            <<<dim3(static_cast<unsigned>(p.groups)), C::THREADS, 0, st>>>(a, p, part, ml);
+            <<<dim3(static_cast<unsigned>(p.groups)), C::THREADS, 0, st>>>(a, p, part, ml, order);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.nsplit == 1)
             return e;
@@ -1228,16 +1296,17 @@ struct Launch {
         else
             join<T, D, 8>(a, p.nsplit, part, ml, st);
         return hipGetLastError();
-        }
     }
 };
 
 template <typename F>
-auto by_type(int D, bool bf16, int64_t R, F f)
+auto by_type(const AttnArgs &a, int D, bool bf16, F f)
 {
+    const int64_t R = static_cast<int64_t>(a.block_len) * (a.H / a.KV);
+    const bool ranged = a.score.ranged();
     if (bf16)
-        return D == 64 ? by_rows<__bf16, 64>(R, f) : by_rows<__bf16, 128>(R, f);
-    return D == 64 ? by_rows<float, 64>(R, f) : by_rows<float, 128>(R, f);
+        return D == 64 ? by_rows<__bf16, 64>(R, ranged, f) : by_rows<__bf16, 128>(R, ranged, f);
+    return D == 64 ? by_rows<float, 64>(R, ranged, f) : by_rows<float, 128>(R, ranged, f);
 }
 
 }  // namespace

@@ -53,9 +53,19 @@ struct Planner {
             keys = std::min(keys, back() + ahead() + TK);
         return (keys + TK - 1) / TK;
     }
+    bool ranged() const { return a.score.ranged(); }
+    // row tiles of rows with ranges are sorted where they take more than one round
+    size_t order_bytes() const
+    {
+        return ranged() && units * nrt > 8 * slots ? static_cast<size_t>((static_cast<int64_t>(a.batch) * nrt * 4 + 255) / 256 * 256)
+                                                   : 0;
+    }
     int64_t candidates(int64_t tiles) const  // 1 to so many ranges come into question
     {
-        return std::max<int64_t>(1, std::min({static_cast<int64_t>(kMostRanges), f32 ? tiles : (tiles + 1) / 2,
+        // rows with ranges of their own may see few of the keys (documents packed into a chunk): their
+        // keys are cut only as far as it takes to fill the GPU once
+        const int64_t fill = ranged() ? (8 * slots + units * nrt - 1) / (units * nrt) : kMostRanges;
+        return std::max<int64_t>(1, std::min({static_cast<int64_t>(kMostRanges), fill, f32 ? tiles : (tiles + 1) / 2,
                                               kMaxGroups / 8 / (units * nrt)}));
     }
     AttnPlan deal(int64_t ns) const  // the parts of a launch with ns ranges
@@ -109,7 +119,10 @@ struct Planner {
         p.by_split = Divisor(ns);
         p.groups = 8ll * p.per_xcd * p.nrt_sub;
         p.ml_bytes = ns > 1 ? ml_bytes(ns) : 0;
-        p.ws_bytes = ns > 1 ? bytes(ns) : 0;
+        p.order_bytes = order_bytes();
+        p.ws_bytes = (ns > 1 ? bytes(ns) : 0) + p.order_bytes;
+        for (int64_t keys = (static_cast<int64_t>(a.max_len) + a.block_len) / TK; keys >> p.order_shift >= 1024;)
+            ++p.order_shift;
         return p;
     }
     size_t ml_bytes(int64_t ns) const { return static_cast<size_t>((units * R * ns * 8 + 255) / 256 * 256); }
@@ -162,7 +175,7 @@ struct Planner {
         lengths(false, 0, g.from);
         lengths(true, g.from, g.to);
         lengths(false, std::max(g.from, g.to), INT64_MAX);
-        return most > 1 ? bytes(most) : 0;
+        return (most > 1 ? bytes(most) : 0) + order_bytes();
     }
 };
 
@@ -188,17 +201,17 @@ struct WorkspaceOf {
 
 AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16)
 {
-    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), PlanOf{a});
+    return by_type(a, D, bf16, PlanOf{a});
 }
 
 size_t attn_workspace(const AttnArgs &a, int D, bool bf16)
 {
-    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), WorkspaceOf{a});
+    return by_type(a, D, bf16, WorkspaceOf{a});
 }
 
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st)
 {
-    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), Launch<kPlain>{a, p, ws, st});
+    return by_type(a, D, bf16, Launch<kPlain>{a, p, ws, st});
 }
 
 }  // namespace bdssm

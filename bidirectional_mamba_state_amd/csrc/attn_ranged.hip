@@ -6,7 +6,7 @@ namespace bdssm {
 
 hipError_t launch_attn_ranged(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st)
 {
-    return by_type(D, bf16, static_cast<int64_t>(a.block_len) * (a.H / a.KV), Launch<kRanged>{a, p, ws, st});
+    return by_type(a, D, bf16, Launch<kRanged>{a, p, ws, st});
 }
 
 }  // namespace bdssm

@@ -629,7 +629,8 @@ bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk
  * Errors as bdssm_attn_step; BDSSM_ERR_UNSUPPORTED also for a cap that is negative or not finite,
  * or for which scale / cap or cap itself is beyond 2^-126 to 2^126 or so. out and workspace must
  * not overlap these arrays. bdssm_attn_step_ex_workspace says what the call needs as
- * bdssm_attn_step_workspace does (of scores, only cap is looked at).
+ * bdssm_attn_step_workspace does; of scores it looks at cap and at whether first and last are given,
+ * not at what they hold: without ranges it is the same.
  */
 typedef struct {
     float cap;
