@@ -519,6 +519,8 @@ def _rows(t, what, dtype, shape):
     if t.dtype != dtype or t.shape != shape:
         _expect(t, what, dtype, shape)
     steps, width = t.stride(), shape[-1]
+    if len(shape) == 3 and steps[2] == 1 and steps[1] == width:
+        return t.data_ptr(), steps[0] if shape[0] > 1 else width * shape[1]
     inside = steps[-1] == 1 or width == 1
     if len(shape) == 3:
         inside = inside and (steps[1] == width or shape[1] == 1)
@@ -526,6 +528,19 @@ def _rows(t, what, dtype, shape):
     if not inside:
         raise ValueError(f"{what}: rows must be contiguous")
     return t.data_ptr(), steps[0] if shape[0] > 1 else width
+
+
+_int32 = None
+
+
+def _expect_int(t, what, shape):
+    """An int32 tensor argument: its shape (a tuple)."""
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    if t.dtype != _int32 or t.shape != shape:
+        _expect(t, what, _int32, shape)
 
 
 def norm_dims(rows, width, dtype, groups=1, eps=1e-5, rows_per_stream=0, kind=NORM_RMS, x_dtype=None):
@@ -750,8 +765,7 @@ def rotary_step(ad, block_len, rotary, q, k, q_out, k_out, lens=None, starts=Non
     ch = _chunk(ad, block_len, q, k, None, starts)
     out = _rotary_out(ad, rotary, ch, q_out, k_out)
     if lens is not None:
-        import torch
-        _expect(lens, "lens", torch.int32, (ad.batch,))
+        _expect_int(lens, "lens", (ad.batch,))
     _check(load().bdssm_rotary_step(ctypes.byref(ad), ctypes.byref(ch), ctypes.byref(rotary.ptrs), _ptr(lens),
                                     ctypes.byref(out), _stream(stream)))
 
@@ -785,12 +799,6 @@ class Pages:
         self.ptrs = PagesPtrs(_ptr(table), _ptr(lens), _ptr(uses))
 
 
-def _expect_ints(pairs):
-    import torch
-    for t, what, shape in pairs:
-        _expect(t, what, torch.int32, shape)
-
-
 def pages_workspace(pd):
     """bdssm_pages_workspace: bytes that serve each of the pages_* calls (SIZE_MAX for dims that they
     would reject)."""
@@ -801,10 +809,12 @@ def pages_advance(pd, pages, block_len, table_out, uses_out, lacking, workspace,
                   stream=None):
     """bdssm_pages_advance: the pages of the next block_len tokens (or of starts) taken, those behind
     the window given back; table_out and uses_out may be the pages' own; lacking [1] int32."""
-    _expect_ints(((table_out, "table_out", (pd.batch, pd.max_pages)), (uses_out, "uses_out", (pd.num_pages,)),
-                  (lacking, "lacking", (1,))))
+    b = pd.batch
+    _expect_int(table_out, "table_out", (b, pd.max_pages))
+    _expect_int(uses_out, "uses_out", (pd.num_pages,))
+    _expect_int(lacking, "lacking", (1,))
     if starts is not None:
-        _expect_ints(((starts, "starts", (pd.batch + 1,)),))
+        _expect_int(starts, "starts", (b + 1,))
     _check(load().bdssm_pages_advance(ctypes.byref(pd), ctypes.byref(pages.ptrs), _ptr(starts), block_len, window, sinks,
                                       _ptr(table_out), _ptr(uses_out), _ptr(lacking), _ptr(workspace), _nbytes(workspace),
                                       _stream(stream)))
@@ -813,9 +823,13 @@ def pages_advance(pd, pages, block_len, table_out, uses_out, lacking, workspace,
 def pages_fork(pd, pages, parents, table_out, lens_out, uses_out, copies, lacking, workspace, stream=None):
     """bdssm_pages_fork: row b becomes the stream of row parents[b] ([batch] int32); copies [batch, 2]
     int32 receives the page copies to be made in every layer (pages_copy), lacking [1] int32."""
-    _expect_ints(((parents, "parents", (pd.batch,)), (table_out, "table_out", (pd.batch, pd.max_pages)),
-                  (lens_out, "lens_out", (pd.batch,)), (uses_out, "uses_out", (pd.num_pages,)),
-                  (copies, "copies", (pd.batch, 2)), (lacking, "lacking", (1,))))
+    b = pd.batch
+    _expect_int(parents, "parents", (b,))
+    _expect_int(table_out, "table_out", (b, pd.max_pages))
+    _expect_int(lens_out, "lens_out", (b,))
+    _expect_int(uses_out, "uses_out", (pd.num_pages,))
+    _expect_int(copies, "copies", (b, 2))
+    _expect_int(lacking, "lacking", (1,))
     _check(load().bdssm_pages_fork(ctypes.byref(pd), ctypes.byref(pages.ptrs), _ptr(parents), _ptr(table_out),
                                    _ptr(lens_out), _ptr(uses_out), _ptr(copies), _ptr(lacking), _ptr(workspace),
                                    _nbytes(workspace), _stream(stream)))
@@ -824,8 +838,11 @@ def pages_fork(pd, pages, parents, table_out, lens_out, uses_out, copies, lackin
 def pages_compact(pd, pages, table_out, uses_out, copies, live, workspace, stream=None):
     """bdssm_pages_compact: the used pages moved to the front of the pool; copies [num_pages // 2, 2]
     int32 receives the moves to be made in every layer (pages_copy), live [1] int32 their number."""
-    _expect_ints(((table_out, "table_out", (pd.batch, pd.max_pages)), (uses_out, "uses_out", (pd.num_pages,)),
-                  (copies, "copies", (pd.num_pages // 2, 2)), (live, "live", (1,))))
+    n = pd.num_pages
+    _expect_int(table_out, "table_out", (pd.batch, pd.max_pages))
+    _expect_int(uses_out, "uses_out", (n,))
+    _expect_int(copies, "copies", (n // 2, 2))
+    _expect_int(live, "live", (1,))
     _check(load().bdssm_pages_compact(ctypes.byref(pd), ctypes.byref(pages.ptrs), _ptr(table_out), _ptr(uses_out),
                                       _ptr(copies), _ptr(live), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
@@ -833,9 +850,9 @@ def pages_compact(pd, pages, table_out, uses_out, copies, live, workspace, strea
 def pages_copy(ad, cache, copies, stream=None):
     """bdssm_pages_copy: the pages of copies [n, 2] int32 (source, destination) copied within one
     layer's pools (a KvCache)."""
-    _expect_ints(((copies, "copies", (copies.shape[0], 2)),))
-    _check(load().bdssm_pages_copy(ctypes.byref(ad), ctypes.byref(cache.ptrs), _ptr(copies), copies.shape[0],
-                                   _stream(stream)))
+    n = copies.shape[0]
+    _expect_int(copies, "copies", (n, 2))
+    _check(load().bdssm_pages_copy(ctypes.byref(ad), ctypes.byref(cache.ptrs), _ptr(copies), n, _stream(stream)))
 
 
 # ------------------------------------------------------------------ data movement helpers

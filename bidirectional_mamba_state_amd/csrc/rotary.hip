@@ -68,10 +68,15 @@ __device__ __forceinline__ void turn_pair(T &a, T &b, float2 t)
 }
 
 // A workgroup takes `tok` tokens of one stream. The scaled cosines and sines of their pairs are
-// made once, in LDS, for all heads; then the threads walk the units of (token, head): queries,
-// keys, values. A unit is loaded before the one in front of it is stored, the first before the
-// cosines are made.
-template <typename T, int LAYOUT, bool APPEND>
+// made once, in LDS, for all heads; the threads walk the units of (token, head): queries, keys,
+// values. Bound by the rows' bytes: a step of 34,000 tokens of 20 + 4 heads x 128 takes 62 us, 6.8
+// TB/s both ways (a large copy by the library: 4.9), with values and into pages 78 us, 6.3. What that
+// took: four pieces of a thread in flight (two: 122 us), 4 tokens a workgroup (16, whose first loads
+// nothing covers: 112 us; eight pieces in flight no better), and, where the outputs are more than the
+// L2s hold, stores that do not stay in them (STREAM; 101 us without). One block of 32: 2.9 us, the
+// launch and the way to the stream's length. Halves that end inside a piece go a pair a thread, 2.4
+// TB/s.
+template <typename T, int LAYOUT, bool APPEND, bool STREAM>
 __global__ __launch_bounds__(256) void k_rotary(RotaryArgs r)
 {
     constexpr int E = 16 / sizeof(T);
@@ -141,22 +146,30 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs r)
         }
         return d;
     };
+    auto put = [](T *to, const Piece<T> &p) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        if constexpr (STREAM)
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, p), reinterpret_cast<u32x4 *>(to));
+        else
+            *reinterpret_cast<Piece<T> *>(to) = p;
+    };
     auto store_at = [&](T *to, const Unit &x, const Data &d) {
         if constexpr (LAYOUT == kSingle) {
             to[0] = d.a.v[0];
             if (is_pair(x))
                 to[pairs] = d.b.v[0];
         } else {
-            *reinterpret_cast<Piece<T> *>(to) = d.a;
+            put(to, d.a);
             if (is_pair(x))
-                *reinterpret_cast<Piece<T> *>(to + pairs) = d.b;
+                put(to + pairs, d.b);
         }
     };
     auto store = [&](const Unit &x, Data d) {
         if (APPEND && x.head >= r.q_heads + a.KV) {
             if (slots[x.i] >= 0)
-                *reinterpret_cast<Piece<T> *>(static_cast<T *>(a.vp) + slots[x.i] +
-                                              static_cast<int64_t>(x.head - r.q_heads - a.KV) * page * r.headdim + x.u * E) = d.a;
+                put(static_cast<T *>(a.vp) + slots[x.i] +
+                        static_cast<int64_t>(x.head - r.q_heads - a.KV) * page * r.headdim + x.u * E,
+                    d.a);
             return;
         }
         const float2 *t = turn + x.i * pairs;
@@ -177,13 +190,18 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs r)
             store_at(static_cast<T *>(a.kp) + slots[x.i] + static_cast<int64_t>(x.head - r.q_heads) * page * r.headdim + c, x, d);
     };
 
-    int x = threadIdx.x;
-    Unit now{};
-    Data d;
-    if (x < total) {
-        now = unit(x);
-        d = load(now);
-    }
+    // U units of a thread are loaded before the first of them is stored, the first U before the cosines
+    // are made
+    constexpr int U = LAYOUT == kTwoPieces ? 2 : 4;
+    Data d[U];
+    auto load_from = [&](int x0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int x = x0 + 256 * k;
+            d[k] = load(unit(x < total ? x : total - 1));
+        }
+    };
+    load_from(threadIdx.x);
     for (int y = threadIdx.x; y < n * pairs; y += 256) {
         const int i = r.by_pairs(y), f = y - i * pairs;
         const int64_t p = r.positions ? r.positions[s.row0 + i0 + i] : static_cast<int64_t>(s.len) + i0 + i;
@@ -198,28 +216,34 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs r)
                                  : (static_cast<int64_t>(pg) * a.KV * page + (j & (page - 1))) * r.headdim;
     }
     __syncthreads();
-    while (x < total) {
-        const int next = x + 256;
-        Unit then{};
-        Data ahead;
-        if (next < total) {
-            then = unit(next);
-            ahead = load(then);
-        }
-        store(now, d);
-        x = next, now = then, d = ahead;
+    for (int x0 = threadIdx.x; x0 < total; x0 += 256 * U) {
+        if (x0 != static_cast<int>(threadIdx.x))
+            load_from(x0);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (x0 + 256 * k < total)
+                store(unit(x0 + 256 * k), d[k]);
     }
 }
 
-template <typename T, bool APPEND>
+template <typename T, bool APPEND, bool STREAM>
 void launch(const RotaryArgs &r, Layout layout, dim3 grid, size_t lds, hipStream_t st)
 {
     if (layout == kPairsInPiece)
-        k_rotary<T, kPairsInPiece, APPEND><<<grid, 256, lds, st>>>(r);
+        k_rotary<T, kPairsInPiece, APPEND, STREAM><<<grid, 256, lds, st>>>(r);
     else if (layout == kTwoPieces)
-        k_rotary<T, kTwoPieces, APPEND><<<grid, 256, lds, st>>>(r);
+        k_rotary<T, kTwoPieces, APPEND, STREAM><<<grid, 256, lds, st>>>(r);
     else
-        k_rotary<T, kSingle, APPEND><<<grid, 256, lds, st>>>(r);
+        k_rotary<T, kSingle, APPEND, false><<<grid, 256, lds, st>>>(r);
+}
+
+template <typename T, bool APPEND>
+void launch(const RotaryArgs &r, Layout layout, dim3 grid, size_t lds, bool stream, hipStream_t st)
+{
+    if (stream)
+        launch<T, APPEND, true>(r, layout, grid, lds, st);
+    else
+        launch<T, APPEND, false>(r, layout, grid, lds, st);
 }
 
 // Rows of a tensor, in bytes.
@@ -307,7 +331,7 @@ bdssm_status run(const bdssm_attn_dims *d, const AttnArgs &a, const AttnRanges &
     r.units = layout == kPairsInPiece ? d->headdim / per16 : layout == kTwoPieces ? (d->headdim - pairs) / per16 : d->headdim - pairs;
     r.rotated = (r.q_heads + (a.k ? d->kv_heads : 0)) * r.units;
     const int64_t most = std::min<int64_t>(a.block_len, a.tokens);  // tokens of a stream
-    r.tok = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, a.tokens / 2048)));
+    r.tok = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(layout == kTwoPieces ? 2 : 4, a.tokens / 2048)));
     r.by_pairs = Divisor(pairs), r.by_unit = Divisor(r.units);
     r.by_token = Divisor(r.rotated + (append ? d->kv_heads * d->headdim / per16 : 0));
     const int64_t blocks = std::max<int64_t>(1, (most + r.tok - 1) / r.tok);  // one is left to write lens_out
@@ -315,10 +339,12 @@ bdssm_status run(const bdssm_attn_dims *d, const AttnArgs &a, const AttnRanges &
         return BDSSM_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks), a.batch);
     const size_t lds = static_cast<size_t>(r.tok) * (pairs + 1) * 8;
+    // the eight L2s hold 32 MB
+    const bool stream = a.tokens * ((r.q_heads ? qw : 0) + (a.k ? kw : 0)) * e > 32 << 20;
     if (d->dtype == BDSSM_BF16)
-        append ? launch<__bf16, true>(r, layout, grid, lds, st) : launch<__bf16, false>(r, layout, grid, lds, st);
+        append ? launch<__bf16, true>(r, layout, grid, lds, stream, st) : launch<__bf16, false>(r, layout, grid, lds, stream, st);
     else
-        append ? launch<float, true>(r, layout, grid, lds, st) : launch<float, false>(r, layout, grid, lds, st);
+        append ? launch<float, true>(r, layout, grid, lds, stream, st) : launch<float, false>(r, layout, grid, lds, stream, st);
     return launched(hipGetLastError());
 }
 
