@@ -2,12 +2,12 @@
 // (bdssm_pages_fork), moving the used pages to the front (bdssm_pages_compact) and copying pages
 // (bdssm_pages_copy).
 //
-// The first three are three launches each. The first takes a snapshot of which pages are free, one
-// bit a page, with a count per chunk of the pool, and counts what each stream needs; the second
-// lists the free pages in order; in the third every stream finds its place among the needs (the sum
-// of those in front of it) and takes its pages from the list. Nothing is handed out by an atomic
-// counter, so that results depend on the contents alone; the uses of pages are counted by integer
-// atomics, whose sum has no order. The snapshot lets uses_out be uses itself.
+// The first launch of each takes a snapshot of which pages are free, one bit a page, with a count per
+// chunk of the pool, and counts what each stream needs. In the second every stream finds its place
+// among the needs (the sum of those in front of it) and the free pages of those ranks (free_pages);
+// a compaction lists them first, in a launch of its own. Nothing is handed out by an atomic counter,
+// so that results depend on the contents alone; the uses of pages are counted by integer atomics,
+// whose sum has no order. The snapshot lets uses_out be uses itself. Small pools: one launch, below.
 #include <limits.h>
 
 #include <algorithm>
@@ -30,7 +30,7 @@ struct PoolArgs {
     uint64_t *bits;  // [chunks][kWords]: the page is free
     int *counts;     // [chunks] free pages
     int *needs;      // [batch]
-    int *list;       // [num_pages] free pages in order
+    int *list;       // [num_pages] compact: free pages in order
     int *map;        // [num_pages] compact: which move a page is, or -1
     int *moves;      // [1] compact: number of moves
 };
@@ -156,19 +156,41 @@ __device__ __forceinline__ int words_before(uint64_t word, int before)
     return before + n - own;
 }
 
-// Free pages of a chunk into the list.
-__global__ __launch_bounds__(256) void k_list(PoolArgs a)
+// The free pages of ranks [from, from + n) into LDS (n up to kTake; -1 past the last), by a workgroup:
+// the chunks that hold them by a running sum of the counts, their words by one lane each.
+constexpr int kTake = 1024;
+
+__device__ __forceinline__ void free_pages(const PoolArgs &a, int from, int n, int *out, int *lds)
 {
-    __shared__ int lds[4];
-    const int chunk = blockIdx.x, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const uint64_t mine = a.bits[static_cast<int64_t>(chunk) * kWords + lane];
-    const int ranks = words_before(mine, sum_of(a.counts, chunk, lds));
-    for (int i = w; i < kWords; i += 4) {
-        const uint64_t word = __shfl(mine, i);
-        const int rank = __shfl(ranks, i);
-        if (word >> lane & 1)
-            a.list[rank + __popcll(word & ((uint64_t{1} << lane) - 1))] = chunk * kChunk + 64 * i + lane;
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    __syncthreads();  // `out` may still be read
+    for (int i = threadIdx.x; i < n; i += 256)
+        out[i] = -1;
+    for (int c0 = 0, before = 0; c0 < a.chunks && before < from + n; c0 += 256) {
+        const int c = c0 + threadIdx.x, count = c < a.chunks ? a.counts[c] : 0;
+        int sum = count;
+#pragma unroll
+        for (int y = 1; y < 64; y *= 2) {
+            const int o = __shfl_up(sum, y);
+            sum += lane >= y ? o : 0;
+        }
+        __syncthreads();
+        if (lane == 63)
+            lds[w] = sum;
+        __syncthreads();
+        int first = before + sum - count;  // rank of the chunk's first
+        for (int x = 0; x < w; ++x)
+            first += lds[x];
+        before += lds[0] + lds[1] + lds[2] + lds[3];
+        for (uint64_t hits = __ballot(count > 0 && first < from + n && first + count > from); hits; hits &= hits - 1) {
+            const int l = __builtin_ctzll(hits), chunk = c0 + 64 * w + l;
+            uint64_t word = a.bits[static_cast<int64_t>(chunk) * kWords + lane];
+            for (int r = words_before(word, __shfl(first, l)); word && r < from + n; ++r, word &= word - 1)
+                if (r >= from)
+                    out[r - from] = chunk * kChunk + 64 * lane + __builtin_ctzll(word);
+        }
     }
+    __syncthreads();
 }
 
 // A row's part [from, to) of `parts`.
@@ -184,7 +206,7 @@ __device__ __forceinline__ Span part_of(const PoolArgs &a, int part)
 // first part's, so that none is ranked by a table that another workgroup has begun to fill.
 __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
 {
-    __shared__ int lds[4];
+    __shared__ int lds[4], list[kTake];
     const int b = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     if (b >= a.p.batch) {  // no streams
         if (threadIdx.x == 0)
@@ -215,8 +237,14 @@ __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
     }
     if (s.from >= s.to)
         return;
-    int place = sum_of(a.p.needs, b, lds);
+    const int place = sum_of(a.p.needs, b, lds), own = a.p.needs[b];
+    int taken = 0, first = 0, listed = 0;  // of the stream's needs: met, and listed [first, listed)
     for (int i0 = s.from; i0 < s.to; i0 += 256) {
+        if (taken + 256 > listed && listed < own) {  // the next 256 entries may need more than are listed
+            listed = taken + kTake < own ? taken + kTake : own;
+            free_pages(a.p, place + taken, listed - taken, list, lds);
+            first = taken;
+        }
         const int i = i0 + threadIdx.x;
         const int e = i < s.to ? in[i] : 0;
         const bool empty = i < s.to && !is_page(a.p, e);
@@ -225,12 +253,12 @@ __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
         if (lane == 0)
             lds[w] = __popcll(word);
         __syncthreads();
-        int r = place + __popcll(word & ((uint64_t{1} << lane) - 1));
+        int r = taken + __popcll(word & ((uint64_t{1} << lane) - 1));
         for (int x = 0; x < w; ++x)
             r += lds[x];
-        place += lds[0] + lds[1] + lds[2] + lds[3];
+        taken += lds[0] + lds[1] + lds[2] + lds[3];
         if (empty) {
-            const int e_new = r < free ? a.p.list[r] : -1;
+            const int e_new = list[r - first];
             if (e_new >= 0)
                 atomicAdd(&a.p.uses_out[e_new], 1);
             out[i] = e_new;
@@ -272,7 +300,7 @@ __global__ __launch_bounds__(256) void k_fork_count(ForkArgs a)
 
 __global__ __launch_bounds__(256) void k_fork_rows(ForkArgs a)
 {
-    __shared__ int lds[4];
+    __shared__ int lds[4], list[1];
     if (a.p.batch == 0) {
         if (threadIdx.x == 0)
             a.lacking[0] = 0;
@@ -288,8 +316,8 @@ __global__ __launch_bounds__(256) void k_fork_rows(ForkArgs a)
     if (blockIdx.x == 0 || (need && whole >= part.from && whole < part.to)) {
         const int free = sum_of(a.p.counts, a.p.chunks, lds);
         if (need) {
-            const int place = sum_of(a.p.needs, b, lds);
-            fresh = place < free ? a.p.list[place] : -1;
+            free_pages(a.p, sum_of(a.p.needs, b, lds), 1, list, lds);
+            fresh = list[0];
         }
         if (blockIdx.x == 0) {
             const int all = b == 0 ? sum_of(a.p.needs, a.p.batch, lds) : 0;
@@ -404,10 +432,10 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a)
 }
 
 // ---- one workgroup
-// The same calls where the pool, the table and the streams are small: one launch instead of three,
-// since three cost more than the work (streams of 64 tokens: 11 us from the host in three, see the
-// limits at kSmallPages). Free pages and uses are held in LDS.
+// The same calls where the pool, the table and the streams are small: one launch, since more cost more
+// than the work. Free pages and uses are held in LDS.
 constexpr int kSmallPages = 16384, kSmallRows = 1024, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int64_t kSmallTake = 24576, kSmallCompact = 49152;
 
 struct Small {
     int list[kSmallPages];  // free pages in order; compact: where a page goes, from page n on
@@ -709,11 +737,12 @@ bdssm_status check_pages_dims(const bdssm_pages_dims *d)
     return BDSSM_OK;
 }
 
-// Whether one workgroup takes a call. In LDS fit 16,384 pages and 1,024 streams; a table of up to
-// 65,536 entries is 64 turns of the workgroup.
-bool small(const bdssm_pages_dims *d)
+// Whether one workgroup takes a call: what it holds in LDS, and as long as pages and table entries
+// together are no more than `most` (measured below).
+bool small(const bdssm_pages_dims *d, int64_t most)
 {
-    return d->num_pages <= kSmallPages && d->batch <= kSmallRows && static_cast<int64_t>(d->batch) * d->max_pages <= 65536;
+    return d->num_pages <= kSmallPages && d->batch <= kSmallRows &&
+           d->num_pages + static_cast<int64_t>(d->batch) * d->max_pages <= most;
 }
 
 int64_t chunks_of(const bdssm_pages_dims *d) { return (static_cast<int64_t>(d->num_pages) + kChunk - 1) / kChunk; }
@@ -827,14 +856,12 @@ extern "C" bdssm_status bdssm_pages_advance(const bdssm_pages_dims *dims, const 
     a.starts = starts, a.block_len = block_len, a.window = window, a.sinks = sinks, a.lacking = lacking;
     hipStream_t st = static_cast<hipStream_t>(stream);
     // a stream's new entries are one thread's there
-    if (small(dims) && block_len / dims->page_size <= 64) {
+    if (small(dims, kSmallTake) && block_len / dims->page_size <= 64) {
         k_advance_small<<<1, kSmallThreads, 0, st>>>(a, Divisor(std::max(1, dims->max_pages)));
         return launched(hipGetLastError());
     }
     if (a.p.chunks + dims->batch > 0)
         k_advance_count<<<a.p.chunks + dims->batch, 256, 0, st>>>(a);
-    if (a.p.chunks > 0)
-        k_list<<<a.p.chunks, 256, 0, st>>>(a.p);
     k_advance_rows<<<dim3(a.p.row_parts, std::max(1, dims->batch)), 256, 0, st>>>(a);
     return launched(hipGetLastError());
 }
@@ -853,15 +880,13 @@ extern "C" bdssm_status bdssm_pages_fork(const bdssm_pages_dims *dims, const bds
         return rc;
     a.parents = parents, a.lens_out = lens_out, a.copies = copies, a.lacking = lacking;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (small(dims)) {
+    if (small(dims, kSmallTake)) {
         k_fork_small<<<1, kSmallThreads, 0, st>>>(a, Divisor(std::max(1, dims->max_pages)));
         return launched(hipGetLastError());
     }
     const int rows = (dims->batch + 3) / 4;
     if (a.p.chunks + rows > 0)
         k_fork_count<<<a.p.chunks + rows, 256, 0, st>>>(a);
-    if (a.p.chunks > 0)
-        k_list<<<a.p.chunks, 256, 0, st>>>(a.p);
     k_fork_rows<<<dim3(a.p.row_parts, std::max(1, dims->batch)), 256, 0, st>>>(a);
     return launched(hipGetLastError());
 }
@@ -881,7 +906,7 @@ extern "C" bdssm_status bdssm_pages_compact(const bdssm_pages_dims *dims, const 
         return rc;
     a.copies = copies, a.live = live;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (small(dims)) {
+    if (small(dims, kSmallCompact)) {
         k_compact_small<<<1, kSmallThreads, 0, st>>>(a);
         return launched(hipGetLastError());
     }
