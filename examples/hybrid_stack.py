@@ -4,6 +4,7 @@ norms. Random weights, hidden vectors instead of tokens (no embedding and no out
 
     python examples/hybrid_stack.py            the 350M shape, 4 streams, prefix 4,096
     python examples/hybrid_stack.py --tiny     a few small layers
+    python examples/hybrid_stack.py --samples 4 --rotary --cap 30    one prompt, four continuations
 
 The stack alternates groups of Mamba layers with one attention layer. Between layers the
 residual stream is updated by bdssm.residual_norm (the layer's output norm, the timestep's gate
@@ -15,6 +16,12 @@ are torch's.
             states and the pages (no timestep: the cache must not depend on it)
   denoise   one step of the active block: block steps and attention read the caches, write none
   commit    the clean pass over the finished block: states advance, keys and values are appended
+  fork      streams rearranged or continued several times: states are gathered, pages shared
+  compact   the pages in use moved to the front of the pools
+
+Options: rotary positions on queries and keys, a cap on the attention scores, a bias by distance;
+and `managed`, pages taken when a block needs them and given back when its window has left them
+(else every stream holds its pages from the start).
 """
 import argparse
 import math
@@ -100,15 +107,23 @@ class AttentionLayer:
         mask = m.mask if mode == "denoise" else m.block_mask
         out = torch.empty((n, H, 64), dtype=u.dtype, device="cuda")
         ws = m.ws if tokens == BLOCK else m.workspace(tokens, self.cache.max_len, mask)
-        bdssm.attn_step(m.attn, tokens, q, k, v, self.cache, mask, out, ws)
-        if mode != "denoise":
+        if m.rotary is not None:  # in place; a commit's keys go into the pages on the way
+            if mode == "denoise":
+                bdssm.rotary_step(m.attn, tokens, m.rotary, q, k, q, k, lens=m.lens[0])
+            else:
+                bdssm.rotary_append(m.attn, tokens, m.rotary, q, k, v, self.cache, q, k, m.lens[1])
+        if m.scores is not None:
+            bdssm.attn_step_ex(m.attn, tokens, q, k, v, self.cache, mask, m.scores, out, ws)
+        else:
+            bdssm.attn_step(m.attn, tokens, q, k, v, self.cache, mask, out, ws)
+        if mode != "denoise" and m.rotary is None:
             bdssm.kv_append(m.attn, tokens, k, v, self.cache, m.lens[1])
         return out.view(n, -1) @ self.w_out
 
 
 class HybridStack:
     def __init__(self, batch, width, mamba_heads, attn_heads, kv_heads, layers, attn_every, max_tokens, window=0, sinks=0,
-                 seed=0):
+                 seed=0, rotary=False, cap=0.0, bias=False, managed=False):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.batch, self.width, self.attn_heads, self.kv_heads = batch, width, attn_heads, kv_heads
@@ -117,6 +132,17 @@ class HybridStack:
         self.table = torch.randperm(self.pages, generator=g, device="cuda").to(torch.int32).view(batch, per)
         self.lens = [torch.zeros(batch, dtype=torch.int32, device="cuda") for _ in range(2)]
         self.length = 0  # the same for every stream here
+        self.rotary = bdssm.Rotary(bdssm.rotary_turns(64)) if rotary else None
+        slopes = torch.exp2(-8.0 * torch.arange(1, attn_heads + 1, device="cuda") / attn_heads) if bias else None
+        self.scores = bdssm.AttnScores(cap=cap, slopes=slopes) if cap or bias else None
+        self.window, self.sinks, self.managed = window, sinks, managed
+        self.page_dims = bdssm.page_dims(batch, self.page, self.pages, per)
+        self.uses = torch.ones(self.pages, dtype=torch.int32, device="cuda")
+        if managed:
+            self.table.fill_(-1)
+            self.uses.zero_()
+        self.lacking = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.pages_ws = torch.empty(bdssm.pages_workspace(self.page_dims), dtype=torch.uint8, device="cuda")
         self.attn = bdssm.attn_dims(batch, attn_heads, kv_heads, 64, bdssm.BF16, self.page)
         self.mask = bdssm.attn_mask(0.125, 0, window, sinks)          # inside the active block: no order
         self.block_mask = bdssm.attn_mask(0.125, BLOCK, window, sinks)  # clean tokens: by blocks
@@ -128,7 +154,48 @@ class HybridStack:
         self.w_time = self.weight(g, 64, 3 * width * layers)
 
     def workspace(self, tokens, max_len, mask):
-        return torch.empty(bdssm.attn_step_workspace(self.attn, tokens, max_len, mask), dtype=torch.uint8, device="cuda")
+        need = bdssm.attn_step_workspace(self.attn, tokens, max_len, mask) if self.scores is None else \
+            bdssm.attn_step_ex_workspace(self.attn, tokens, max_len, mask, self.scores)
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def books(self):
+        return bdssm.Pages(self.page_dims, self.table, self.lens[0], self.uses)
+
+    def advance(self, tokens):
+        """Pages of the next `tokens` tokens taken, those behind the window given back."""
+        bdssm.pages_advance(self.page_dims, self.books(), tokens, self.table, self.uses, self.lacking, self.pages_ws,
+                            self.window, self.sinks)
+
+    def attention_layers(self):
+        return [layer for layer in self.layers if isinstance(layer, AttentionLayer)]
+
+    def _take(self, table, copies):
+        """A new table, and the page copies that it asks for."""
+        self.table.copy_(table)
+        for layer in self.attention_layers():
+            bdssm.pages_copy(self.attn, layer.cache, copies)
+
+    def fork(self, parents):
+        """Stream b becomes a continuation of stream parents[b] (an int32 tensor); pages have to be
+        managed."""
+        table, copies = torch.empty_like(self.table), torch.empty((self.batch, 2), dtype=torch.int32, device="cuda")
+        bdssm.pages_fork(self.page_dims, self.books(), parents, table, self.lens[1], self.uses, copies, self.lacking,
+                         self.pages_ws)
+        self._take(table, copies)
+        self.lens[0].copy_(self.lens[1])
+        rows = parents.long()
+        for layer in self.layers:
+            if isinstance(layer, MambaLayer):
+                layer.state.copy_(layer.state[rows])
+                bdssm.state_ops(layer.dims, layer.state, layer.ops)
+
+    def compact(self):
+        """The pages in use moved to the front of the pools; returns their number (on the device)."""
+        copies = torch.empty((self.pages // 2, 2), dtype=torch.int32, device="cuda")
+        live = torch.empty_like(self.lacking)
+        bdssm.pages_compact(self.page_dims, self.books(), self.table, self.uses, copies, live, self.pages_ws)
+        self._take(self.table, copies)
+        return live
 
     def weight(self, g, rows, cols):
         return (torch.randn((rows, cols), generator=g, device="cuda") / math.sqrt(rows)).bfloat16()
@@ -165,12 +232,16 @@ class HybridStack:
         return x
 
     def prefill(self, x, tokens):
+        if self.managed:
+            self.advance(tokens)
         return self.forward(x, tokens, "prefill")
 
     def denoise(self, x, t):
         return self.forward(x, x.shape[0] // self.batch, "denoise", t)
 
     def commit(self, x):
+        if self.managed:
+            self.advance(x.shape[0] // self.batch)
         return self.forward(x, x.shape[0] // self.batch, "commit")
 
 
@@ -180,15 +251,24 @@ def main():
     ap.add_argument("--blocks", type=int, default=2)
     ap.add_argument("--steps", type=int, default=8, help="denoising steps of a block")
     ap.add_argument("--window", type=int, default=0, help="sliding window of the attention layers (with 4 sinks)")
+    ap.add_argument("--rotary", action="store_true", help="rotary positions in the attention layers")
+    ap.add_argument("--cap", type=float, default=0.0, help="cap of the attention scores")
+    ap.add_argument("--bias", action="store_true", help="attention scores biased by distance")
+    ap.add_argument("--samples", type=int, default=0, help="continuations of one prompt, their pages shared")
     a = ap.parse_args()
     batch, prefix = (2, 256) if a.tiny else (4, 4096)
+    batch = a.samples or batch
     shape = dict(width=256, mamba_heads=8, attn_heads=4, kv_heads=2, layers=4, attn_every=3) if a.tiny else \
         dict(width=1024, mamba_heads=32, attn_heads=16, kv_heads=4, layers=24, attn_every=5)
-    model = HybridStack(batch, max_tokens=prefix + a.blocks * BLOCK, window=a.window, sinks=4 if a.window else 0, **shape)
+    model = HybridStack(batch, max_tokens=prefix + a.blocks * BLOCK, window=a.window, sinks=4 if a.window else 0,
+                        rotary=a.rotary, cap=a.cap, bias=a.bias, managed=a.samples > 0, **shape)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     rows = lambda n: torch.randn((batch * n, model.width), generator=g, device="cuda")  # noqa: E731
     model.prefill(rows(prefix), prefix)
+    if a.samples:
+        model.fork(torch.zeros(batch, dtype=torch.int32, device="cuda"))
+        print(f"{int((model.uses > 0).sum())} pages for {batch} continuations of one prompt", flush=True)
     for block in range(a.blocks):
         noisy = rows(BLOCK)
         torch.cuda.synchronize()

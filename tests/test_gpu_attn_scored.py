@@ -177,6 +177,35 @@ def test_documents(dtype, block, kind):
     Scored(lens, counts, last=last, block=block, dtype=dtype, **more).check("last only")
 
 
+@pytest.mark.parametrize("dtype,D,streams,block", [(BF16, 64, 33, 0), (BF16, 128, 22, 1), (F32, 64, 11, 1)])
+def test_sorted_row_tiles(dtype, D, streams, block):
+    """More row tiles than the GPU takes at once, sorted by what they walk (tests/scored_plan_check.cc has
+    these shapes): documents, padding, streams of none or few tokens."""
+    _case(f"sorted dtype {dtype} D {D}")
+    lens = [(i * 37) % 90 for i in range(streams)]
+    counts = [0 if i == 5 else 3 if i == 6 else 300 - (i * 13) % 200 if i else 300 for i in range(streams)]
+    first, last = documents(lens, counts, [3, 4, 40, 64, 100, 150, 152, 200, 215, 300])
+    at = 0
+    for n in counts:
+        for i in range(max(0, n - n // 16), n):
+            first[at + i] = last[at + i] = 0
+        at += n
+    c = Scored(lens, counts, H=8, KV=8, D=D, dtype=dtype, first=first, last=last, block=block, cap=20.0)
+    assert c.workspace() is not None
+    c.check("sorted")
+    assert (c.run() == c.run()).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ranges_over_a_cut_cache(dtype):
+    """Few rows on a long cache, their keys cut into ranges of which some hold nothing that they see."""
+    _case(f"cut cache dtype {dtype}")
+    for first, last in (([0, 2900, 100], [3000, 3003, 101]), ([2000, 2000, 2000], [2010, 2001, 2000])):
+        c = Scored([3000], [3], H=2, KV=1, dtype=dtype, first=first, last=last, slopes=[0.5, 0.1])
+        assert c.workspace() is not None
+        c.check("cut")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (0, 40), (30, 5), (64, 100)])
 @pytest.mark.parametrize("own_keys", [True, False])

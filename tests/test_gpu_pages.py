@@ -184,6 +184,11 @@ def test_advance_by_many_pages(in_place):
     same(Device(m).advance([14000, 1040, 5000], 0, 0, in_place), m.advance([14000, 1040, 5000]), "many")
     m = random_cache(g, 2, 90, 400, 16)
     same(Device(m).advance([64 * 16 + 15, 3], 0, 0, in_place), m.advance([64 * 16 + 15, 3]), "at the limit")
+    m = random_cache(g, 3, 3000, 9000, 16, gaps=0.3)  # more than a workgroup lists at a time
+    m.lens[:] = [0, 700, 0]
+    m.table[2] = -1
+    m.uses = np.bincount(m.table[(m.table >= 0) & (m.table < m.P)], minlength=m.P).astype(np.int32)
+    same(Device(m).advance([40000, 33000, 48000], 0, 0, in_place), m.advance([40000, 33000, 48000]), "thousands")
 
 
 @pytest.mark.parametrize("in_place", [False, True])
