@@ -145,6 +145,21 @@ def test_caps(cap, qscale, dtype):
     Scored([100], [20], cap=cap, qscale=qscale, dtype=dtype).check("cap")
 
 
+@pytest.mark.parametrize("cap", [0.5, 8.0, 30.0, 50.0, 256.0, 257.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_on_every_bf16_shape(cap, D):
+    """Small scores (made along with the weights at headdim 128), large ones and both in one tile, in the
+    shapes for few rows, for many, and for many with ranges."""
+    _case(f"caps D {D} cap {cap}")
+    for qscale in (0.05, 2.0, 8.0):
+        Scored([200], [3], H=4, KV=1, D=D, cap=cap, qscale=qscale).check("few rows")
+        Scored([130], [150], H=2, KV=1, D=D, cap=cap, qscale=qscale, block=1).check("many rows")
+        Scored([130], [90], H=2, KV=1, D=D, cap=cap, qscale=qscale, first=[64] * 90).check("with ranges")
+    c = Scored([200], [40], H=4, KV=1, D=D, cap=cap, qscale=0.05)
+    c.q[7:20] *= 100  # some rows' scores are large
+    c.check("mixed rows")
+
+
 @pytest.mark.parametrize("slope", [0.0, 1e-4, 0.7, 30.0, -0.01])
 @pytest.mark.parametrize("block,window,sinks", [(0, 0, 0), (1, 0, 0), (32, 50, 4)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
