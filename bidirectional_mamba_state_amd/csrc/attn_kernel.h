@@ -162,7 +162,7 @@ struct RowRangeEx : RowRange {
 struct Sight {
     int lo, hi, first;
 };
-constexpr int kNever = INT_MAX;  // lo and first of a token that attends to nothing; its hi is 0
+constexpr int kNever = INT_MAX;  // lo and first of a token whose range leaves it nothing; its hi is 0
 
 template <bool EX>
 __device__ __forceinline__ Sight sight_of(const AttnArgs &a, const AttnStream &s, int end, int prefix, int tok)
@@ -184,7 +184,8 @@ __device__ __forceinline__ Sight sight_of(const AttnArgs &a, const AttnStream &s
             const int last = within(a.score.last[s.row0 + tok]);
             x.hi = x.hi < last ? x.hi : last;
         }
-        if (x.lo >= x.hi && x.first >= (x.hi < a.sinks ? x.hi : a.sinks))
+        // without ranges the bounds are left to grow with the token, which the kernel relies on there
+        if ((a.score.first || a.score.last) && x.lo >= x.hi && x.first >= (x.hi < a.sinks ? x.hi : a.sinks))
             x = {kNever, 0, kNever};
     }
     return x;

@@ -384,3 +384,17 @@ def test_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), lens
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
+def test_queries_that_a_window_leaves_no_cached_key(dtype, D, kind):
+    """Without keys of the chunk's own a window leaves the first queries some of the cache and the later
+    ones nothing: zeros, beside rows of the same workgroup that see keys."""
+    _case(f"scored cache alone D {D} dtype {dtype} {kind}")
+    for lens, counts, more in [([0, 40, 5], [20, 20, 20], {}), ([100], [70], {}), ([100], [70], dict(block=1)),
+                               ([3000], [12], {}), ([100], [70], dict(prefix=[30]))]:
+        c = scored(lens, counts, kind, dtype=dtype, D=D, own_keys=False, window=10, **more)
+        out = c.run()
+        c.check("cache alone")
+        assert not out[10:20].any()  # row 10 of the first stream looks back to position lens + 1
