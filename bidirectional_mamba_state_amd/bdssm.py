@@ -623,6 +623,7 @@ class KvCache:
         _expect(table, "table", torch.int32, (ad.batch, table.shape[-1]))
         _expect(lens, "lens", torch.int32, (ad.batch,))
         self.k, self.v, self.table, self.lens = k, v, table, lens
+        self.page = (ad.kv_heads, ad.headdim, ad.page_size, ad.dtype)
         self.ptrs = KvCachePtrs(_ptr(k), _ptr(v), _ptr(table), _ptr(lens), k.shape[0], table.shape[1], max_len)
 
     @property
@@ -796,7 +797,13 @@ class Pages:
         _expect(lens, "lens", torch.int32, (pd.batch,))
         _expect(uses, "uses", torch.int32, (pd.num_pages,))
         self.table, self.lens, self.uses = table, lens, uses
+        self.pd, self.sizes = pd, (pd.batch, pd.max_pages, pd.num_pages)
         self.ptrs = PagesPtrs(_ptr(table), _ptr(lens), _ptr(uses))
+
+
+def _pages_of(pd, pages):
+    if pages.pd is not pd and pages.sizes != (pd.batch, pd.max_pages, pd.num_pages):
+        raise ValueError(f"pages: made for (batch, max_pages, num_pages) {pages.sizes}")
 
 
 def pages_workspace(pd):
@@ -809,6 +816,7 @@ def pages_advance(pd, pages, block_len, table_out, uses_out, lacking, workspace,
                   stream=None):
     """bdssm_pages_advance: the pages of the next block_len tokens (or of starts) taken, those behind
     the window given back; table_out and uses_out may be the pages' own; lacking [1] int32."""
+    _pages_of(pd, pages)
     b = pd.batch
     _expect_int(table_out, "table_out", (b, pd.max_pages))
     _expect_int(uses_out, "uses_out", (pd.num_pages,))
@@ -823,6 +831,7 @@ def pages_advance(pd, pages, block_len, table_out, uses_out, lacking, workspace,
 def pages_fork(pd, pages, parents, table_out, lens_out, uses_out, copies, lacking, workspace, stream=None):
     """bdssm_pages_fork: row b becomes the stream of row parents[b] ([batch] int32); copies [batch, 2]
     int32 receives the page copies to be made in every layer (pages_copy), lacking [1] int32."""
+    _pages_of(pd, pages)
     b = pd.batch
     _expect_int(parents, "parents", (b,))
     _expect_int(table_out, "table_out", (b, pd.max_pages))
@@ -838,6 +847,7 @@ def pages_fork(pd, pages, parents, table_out, lens_out, uses_out, copies, lackin
 def pages_compact(pd, pages, table_out, uses_out, copies, live, workspace, stream=None):
     """bdssm_pages_compact: the used pages moved to the front of the pool; copies [num_pages // 2, 2]
     int32 receives the moves to be made in every layer (pages_copy), live [1] int32 their number."""
+    _pages_of(pd, pages)
     n = pd.num_pages
     _expect_int(table_out, "table_out", (pd.batch, pd.max_pages))
     _expect_int(uses_out, "uses_out", (n,))
@@ -850,6 +860,8 @@ def pages_compact(pd, pages, table_out, uses_out, copies, live, workspace, strea
 def pages_copy(ad, cache, copies, stream=None):
     """bdssm_pages_copy: the pages of copies [n, 2] int32 (source, destination) copied within one
     layer's pools (a KvCache)."""
+    if cache.page != (ad.kv_heads, ad.headdim, ad.page_size, ad.dtype):
+        raise ValueError(f"cache: its pages are of (kv_heads, headdim, page_size, dtype) {cache.page}")
     n = copies.shape[0]
     _expect_int(copies, "copies", (n, 2))
     _check(load().bdssm_pages_copy(ctypes.byref(ad), ctypes.byref(cache.ptrs), _ptr(copies), n, _stream(stream)))

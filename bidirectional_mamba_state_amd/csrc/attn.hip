@@ -140,6 +140,9 @@ bdssm_status prepare_scores(const bdssm_attn_scores *s, float scale, bool bf16, 
         return BDSSM_ERR_NULL;
     if (!(s->cap >= 0.f) || s->cap - s->cap != 0.f)  // negative, NaN or infinite
         return BDSSM_ERR_UNSUPPORTED;
+    // with bf16 the products start from the bias over the scale
+    if (s->slopes && !(scale >= 0x1p-64f && scale <= 0x1p64f))
+        return BDSSM_ERR_UNSUPPORTED;
     if (!aligned4(s->slopes) || !aligned4(s->prefix) || !aligned4(s->first) || !aligned4(s->last))
         return BDSSM_ERR_ALIGN;
     AttnScoring &g = a->score;

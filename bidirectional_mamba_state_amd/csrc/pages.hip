@@ -14,7 +14,6 @@
 
 #include "attn.h"
 #include "internal.h"
-#include "wave_ops.h"
 
 namespace bdssm {
 namespace {
@@ -704,8 +703,8 @@ __global__ __launch_bounds__(256) void k_pages_copy(char *k, char *v, const int 
 {
     char *pool = blockIdx.y & 1 ? v : k;
     const int64_t at = (static_cast<int64_t>(blockIdx.y >> 1) * kPieces * 256 + threadIdx.x) * 16;
-    for (int i = blockIdx.x; i < n; i += step) {
-        const int from = copies[2 * static_cast<int64_t>(i)], to = copies[2 * static_cast<int64_t>(i) + 1];
+    for (int64_t i = blockIdx.x; i < n; i += step) {
+        const int from = copies[2 * i], to = copies[2 * i + 1];
         if (from < 0 || to < 0 || from >= num_pages || to >= num_pages || from == to)
             continue;
         const char *src = pool + from * page_bytes;
@@ -853,6 +852,9 @@ extern "C" bdssm_status bdssm_pages_advance(const bdssm_pages_dims *dims, const 
         return rc;
     if (block_len < 0 || window < 0 || sinks < 0)
         return BDSSM_ERR_SHAPE;
+    // entries that new tokens start, of all streams, are counted in 32 bits
+    if (batch * std::min(dims->max_pages, block_len / dims->page_size + 1) > INT_MAX)
+        return BDSSM_ERR_UNSUPPORTED;
     a.starts = starts, a.block_len = block_len, a.window = window, a.sinks = sinks, a.lacking = lacking;
     hipStream_t st = static_cast<hipStream_t>(stream);
     // a stream's new entries are one thread's there

@@ -318,6 +318,9 @@ bdssm_status run(const bdssm_attn_dims *d, const AttnArgs &a, const AttnRanges &
                 return BDSSM_ERR_ALIAS;
     if (overlap(in.kp, in.vp) || overlap(rl, in.kp) || overlap(rl, in.vp))
         return BDSSM_ERR_ALIAS;
+    const int64_t most = std::min<int64_t>(a.block_len, a.tokens);  // tokens of a stream
+    if (most > 1 << 24)  // threads along x have to fit 32 bits; there a workgroup has two tokens at least
+        return BDSSM_ERR_UNSUPPORTED;
     if (a.batch == 0 || (!append && (a.tokens == 0 || a.block_len == 0)))
         return BDSSM_OK;
     RotaryArgs r{};
@@ -330,13 +333,10 @@ bdssm_status run(const bdssm_attn_dims *d, const AttnArgs &a, const AttnRanges &
     const Layout layout = ro->interleaved ? kPairsInPiece : pairs % per16 == 0 ? kTwoPieces : kSingle;
     r.units = layout == kPairsInPiece ? d->headdim / per16 : layout == kTwoPieces ? (d->headdim - pairs) / per16 : d->headdim - pairs;
     r.rotated = (r.q_heads + (a.k ? d->kv_heads : 0)) * r.units;
-    const int64_t most = std::min<int64_t>(a.block_len, a.tokens);  // tokens of a stream
     r.tok = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(layout == kTwoPieces ? 2 : 4, a.tokens / 2048)));
     r.by_pairs = Divisor(pairs), r.by_unit = Divisor(r.units);
     r.by_token = Divisor(r.rotated + (append ? d->kv_heads * d->headdim / per16 : 0));
     const int64_t blocks = std::max<int64_t>(1, (most + r.tok - 1) / r.tok);  // one is left to write lens_out
-    if (blocks > (1 << 23))  // threads along x have to fit 32 bits
-        return BDSSM_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(blocks), a.batch);
     const size_t lds = static_cast<size_t>(r.tok) * (pairs + 1) * 8;
     // the eight L2s hold 32 MB

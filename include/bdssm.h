@@ -623,12 +623,12 @@ bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk
  * Workgroups skip keys that the ranges of all their rows leave out, so that documents packed
  * into one chunk cost what they cost apart.
  *   cap       0 (none) or > 0, finite
- *   slopes    [nheads] device float32, or NULL
+ *   slopes    [nheads] device float32, finite, or NULL
  *   prefix    [batch] device int32, or NULL
  *   first, last  [tokens] device int32 in the order of chunk rows, each or NULL (0, no end)
  * Errors as bdssm_attn_step; BDSSM_ERR_UNSUPPORTED also for a cap that is negative or not finite,
- * or for which scale / cap or cap itself is beyond 2^-126 to 2^126 or so. out and workspace must
- * not overlap these arrays. bdssm_attn_step_ex_workspace says what the call needs as
+ * or for which scale / cap or cap itself is beyond 2^-126 to 2^126 or so, and for a scale outside
+ * 2^-64 to 2^64 where slopes are given. out and workspace must not overlap these arrays. bdssm_attn_step_ex_workspace says what the call needs as
  * bdssm_attn_step_workspace does; of scores it looks at cap and at whether first and last are given,
  * not at what they hold: without ranges it is the same.
  */
@@ -700,8 +700,9 @@ typedef struct {
  *          positions are given)
  *   out    rows out->q, out->k: the chunk's own rows in place (same address and stride), or rows
  *          that overlap nothing. Slices of the same projection rows do not overlap.
- * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED, BDSSM_ERR_ALIGN, BDSSM_ERR_ALIAS,
- * BDSSM_ERR_HIP, as bdssm_attn_step.
+ * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (also a chunk whose streams may
+ * have more than 2^24 tokens each), BDSSM_ERR_ALIGN, BDSSM_ERR_ALIAS, BDSSM_ERR_HIP, as
+ * bdssm_attn_step.
  */
 bdssm_status bdssm_rotary_step(const bdssm_attn_dims *dims, const bdssm_attn_chunk *chunk, const bdssm_rotary *rotary,
                                const int32_t *lens, const bdssm_rotary_out *out, void *stream);
@@ -736,8 +737,8 @@ bdssm_status bdssm_rotary_append(const bdssm_attn_dims *dims, const bdssm_attn_c
  * No call reads a count that the host does not have: where pages run out, the entries that lack
  * one stay empty (-1) and lacking[0] says how many.
  * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (page_size, batch above 65535,
- * positions past 2^31), BDSSM_ERR_ALIGN (4 bytes; workspace 16), BDSSM_ERR_ALIAS,
- * BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The query returns SIZE_MAX for dims the calls reject.
+ * positions past 2^31, an advance that could need 2^31 pages), BDSSM_ERR_ALIGN (4 bytes;
+ * workspace 16), BDSSM_ERR_ALIAS, BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The query returns SIZE_MAX for dims the calls reject.
  */
 typedef struct {
     int32_t batch;     /* streams */

@@ -38,6 +38,8 @@ def test_attn_step_ex_refusals():
         assert step_ex(s=scores(cap)) == UNSUPPORTED, cap
     assert step_ex(s=scores(1e-37), m=(10.0, 0, 0, 0)) == UNSUPPORTED  # scale / cap is infinite
     at = BASE + 10 * GB
+    for scale in (2.0**-65, 2.0**65):
+        assert step_ex(s=scores(slopes=at), m=(scale, 0, 0, 0)) == UNSUPPORTED
     for name in ("slopes", "prefix", "first", "last"):
         assert step_ex(s=scores(**{name: at + 2})) == ALIGN
         size = dict(slopes=4, prefix=2, first=16, last=16)[name] * 4
@@ -112,6 +114,8 @@ def test_rotary_step_refusals():
     assert rstep(out=rout(k=None)) == rstep(ch=Chunk(k=None)) == rstep(ch=Chunk(q=None, k=None), out=rout(q=None, k=None)) == NULL
     assert rstep(ch=Chunk(tokens=17)) == rstep(ch=Chunk(block_len=-1)) == rstep(ch=Chunk(q_stride=255)) == SHAPE
     assert rstep(d=dims(headdim=80)) == rstep(ch=Chunk(k_stride=(1 << 24) + 8)) == UNSUPPORTED
+    far = (1 << 24) + 1  # tokens of a stream
+    assert rstep(ch=Chunk(tokens=2 * far, block_len=far, k=BASE + 100 * GB), out=rout(BASE + 200 * GB, BASE + 300 * GB)) == UNSUPPORTED
     assert rstep(ch=Chunk(q=BASE + 4)) == rstep(ch=Chunk(k_stride=132)) == rstep(lens=BASE + 2) == ALIGN
     assert rstep(ch=Chunk(tokens=0, block_len=0)) == rstep(d=dims(batch=0), ch=Chunk(tokens=0)) == bdssm.OK
     # slices of one projection: in place, and each beside the other, is no overlap; half a row off is
@@ -246,6 +250,10 @@ def test_pages_refusals_of_each():
     assert lib.bdssm_pages_advance(r(pd()), None, None, 1, 0, 0, *[BASE] * 4, GB, None) == NULL
     assert advance(T=-1) == advance(window=-1) == advance(sinks=-1) == SHAPE
     assert advance(starts=BASE + 10 * GB + 2) == ALIGN
+    # 2^16 - 1 streams that could each need 2^15 + 1 pages
+    far = dict(g=pages(BASE, BASE + 16384 * GB, BASE + 16385 * GB), t=BASE, u=BASE + 16386 * GB, n=BASE + 16387 * GB,
+               ws=BASE + 16388 * GB)
+    assert advance(d=pd(batch=65535, per=1 << 16), T=16 << 15, **far) == UNSUPPORTED
     assert advance(starts=BASE + 3 * GB + 4) == advance(starts=BASE + 6 * GB) == ALIAS
     assert fork(parents=None) == fork(lens=None) == fork(copies=None) == NULL
     assert fork(t=BASE) == fork(lens=BASE + GB) == fork(lens=BASE + 7 * GB) == fork(copies=BASE + 8 * GB - 8) == ALIAS
@@ -286,6 +294,18 @@ def test_binding_checks_shapes_and_types():
         bdssm.pages_fork(pd(), g, ints(3), ints(2, 8), ints(2), ints(100), ints(2, 2), ints(1), None, stream=0)
     with pytest.raises(ValueError):
         bdssm.pages_compact(pd(), g, ints(2, 8), ints(100), ints(49, 2), ints(1), None, stream=0)
+    # bookkeeping and pools that were made for other sizes
+    out = ints(3, 8), ints(100), ints(1)
+    with pytest.raises(ValueError, match="made for"):
+        bdssm.pages_advance(pd(batch=3), g, 1, *out, None, stream=0)
+    with pytest.raises(ValueError, match="made for"):
+        bdssm.pages_fork(pd(batch=3), g, ints(3), ints(3, 8), ints(3), ints(100), ints(3, 2), ints(1), None, stream=0)
+    with pytest.raises(ValueError, match="made for"):
+        bdssm.pages_compact(pd(P=101), g, ints(2, 8), ints(101), ints(50, 2), ints(1), None, stream=0)
+    pool = FakeCuda(torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16))
+    c = bdssm.KvCache(bdssm.attn_dims(2, 4, 2, 64, bdssm.BF16, 16), pool, pool, ints(2, 8), ints(2), 8)
+    with pytest.raises(ValueError, match="its pages are"):
+        bdssm.pages_copy(bdssm.attn_dims(2, 4, 2, 64, bdssm.BF16, 32), c, ints(1, 2), stream=0)
     with pytest.raises(ValueError):
         bdssm.AttnScores(slopes=ints(4))
     with pytest.raises(ValueError):
