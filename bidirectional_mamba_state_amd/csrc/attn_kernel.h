@@ -47,7 +47,10 @@
 //    every tile are a quarter (1,323 us with them, 1,006 without); 880 TFLOP/s on equal streams,
 //    740 on unequal ones (64 x 16-32K tokens, 768 rows: 1.23 ms), where short row tiles leave
 //    wavefronts idle;
-//  - float32: the matrix cores, 100 to 125 TFLOP/s.
+//  - float32: the matrix cores, 100 to 125 TFLOP/s;
+//  - a cap: the vector unit beside them (48 % busy, matrix cores 34 %): the prompt chunk 1.27 ms, the
+//    unequal streams 1.78; a bias: the prompt chunk 1.23 ms, the unequal streams 1.36, where the vector
+//    unit is 69 % busy; both: 1.69 and 2.07 ms.
 // Eight wavefronts of 32 rows, four a SIMD at headdim 64, did better than four of 64 (half the
 // LDS reads, but nothing hides a wavefront's own exponentials: 1340 against 1020 us on the
 // prompt), than a third stage, 128-key tiles or a scheduled overlap inside a wavefront (no

@@ -432,7 +432,9 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a)
 
 // ---- one workgroup
 // The same calls where the pool, the table and the streams are small: one launch, since more cost more
-// than the work. Free pages and uses are held in LDS.
+// than the work. Free pages and uses are held in LDS. Limits of pages and table entries together: an
+// advance of few takes 4.9 us here and 9.1 as two launches, of 16,000 9.0 and 10.7, of 32,000 14.3 and
+// 10.9; a compaction, three launches else, of 32,000 11.6 and 16.6, of 80,000 18.9 and 16.2.
 constexpr int kSmallPages = 16384, kSmallRows = 1024, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
 constexpr int64_t kSmallTake = 24576, kSmallCompact = 49152;
 
@@ -737,7 +739,7 @@ bdssm_status check_pages_dims(const bdssm_pages_dims *d)
 }
 
 // Whether one workgroup takes a call: what it holds in LDS, and as long as pages and table entries
-// together are no more than `most` (measured below).
+// together are no more than `most`.
 bool small(const bdssm_pages_dims *d, int64_t most)
 {
     return d->num_pages <= kSmallPages && d->batch <= kSmallRows &&
