@@ -269,10 +269,11 @@ struct Poly {
 // Bias: a slope times the distance to the key. The softmax does not change when a row's scores
 // move together, so the distance is taken from the nearest position that the row attends to
 // (`from`): where a row sees only far keys, the common part, which float32 would round, is left out.
-__device__ __forceinline__ int bias_from(const Sight &x, int p)
+__device__ __forceinline__ int bias_from(const Sight &x, int p, int sinks)
 {
+    const int hi = x.lo < x.hi || x.hi < sinks ? x.hi : sinks;  // of the sinks where the window leaves nothing
     const int q = p > x.lo ? p : x.lo;
-    return q < x.hi - 1 ? q : x.hi - 1;
+    return q < hi - 1 ? q : hi - 1;
 }
 
 // An infinity or a NaN among the values of a key that some rows of a workgroup attend to reaches
@@ -355,7 +356,7 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional
                 if constexpr (EX) {
                     sj = MODE >= kCapped ? capped(sj, a.score) : sj * (a.scale * kLog2e);
                     if (a.score.slopes)
-                        sj = fmaf(-slope, fabsf(static_cast<float>(bias_from(see, s.len + tok) - j)), sj);
+                        sj = fmaf(-slope, fabsf(static_cast<float>(bias_from(see, s.len + tok, a.sinks) - j)), sj);
                 }
                 float mx = k ? sj * sc : -__builtin_inff();
                 for (int y = 1; y < 64; y *= 2)
@@ -677,7 +678,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     const float sc = RAW ? a.scale * kLog2e : 1.f;  // of scores as `raise` and `weigh` find them
     const bool bias = EX && a.score.slopes;
     float slope = bias ? a.score.slopes[head] * (RAW ? 1.f / a.scale : kLog2e) : 0.f;
-    const int from = bias_from(my, s.len + tok) - 4 * hf;
+    const int from = bias_from(my, s.len + tok, a.sinks) - 4 * hf;
 
     // ---- operand reads. Every lane offset is one opaque value, a single step from its array:
     // the compiler then sees which array a read is from, and does not make it wait for copies

@@ -398,3 +398,16 @@ def test_queries_that_a_window_leaves_no_cached_key(dtype, D, kind):
         out = c.run()
         c.check("cache alone")
         assert not out[10:20].any()  # row 10 of the first stream looks back to position lens + 1
+
+
+@pytest.mark.parametrize("own_keys", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_bias_among_sinks_alone(dtype, own_keys):
+    """Where the window leaves nothing of the range (or of the cache), distances count from the last
+    sink in sight: a steep slope from further back would round the differences away."""
+    _case(f"sinks alone dtype {dtype} own keys {own_keys}")
+    slopes = [2.0, 0.5, 8.0, 0.0]
+    last = [90, 2000, 30, 2**31 - 1, 1999] * 4 if own_keys else None
+    for cap in (0.0, 30.0):
+        Scored([3000], [20], dtype=dtype, window=9, sinks=40, cap=cap, slopes=slopes, last=last, own_keys=own_keys,
+               qscale=0.3).check("sinks alone")
