@@ -34,17 +34,30 @@ struct PoolArgs {
     int *moves;      // [1] compact: number of moves
 };
 
-// sum over a workgroup of 256 threads, in every thread
-__device__ __forceinline__ int block_sum(int v, int *lds)
+// sums over a workgroup of 256 threads, in every thread; lds: 4 N
+template <int N>
+__device__ __forceinline__ void block_sums(int (&v)[N], int *lds)
 {
 #pragma unroll
-    for (int y = 1; y < 64; y *= 2)
-        v += __shfl_xor(v, y);
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int y = 1; y < 64; y *= 2)
+            v[k] += __shfl_xor(v[k], y);
     __syncthreads();  // lds may still be read from an earlier sum
     if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            lds[4 * k + (threadIdx.x >> 6)] = v[k];
     __syncthreads();
-    return lds[0] + lds[1] + lds[2] + lds[3];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        v[k] = lds[4 * k] + lds[4 * k + 1] + lds[4 * k + 2] + lds[4 * k + 3];
+}
+__device__ __forceinline__ int block_sum(int v, int *lds)
+{
+    int x[1] = {v};
+    block_sums(x, lds);
+    return x[0];
 }
 
 // sum of v[0 .. n), by a workgroup
@@ -56,19 +69,27 @@ __device__ __forceinline__ int sum_of(const int *v, int n, int *lds)
     return block_sum(s, lds);
 }
 
-// A chunk of the snapshot, and uses as they go on being counted (none below 0).
+// A chunk of the snapshot, and uses as they go on being counted (none below 0). All of a thread's uses
+// are loaded before the first is stored: in place the compiler would wait for each (5.4 us for the
+// launch that has this, 3.9 so).
 __device__ __forceinline__ void snapshot(const PoolArgs &a, int chunk, int *lds)
 {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int n = 0;
-    for (int i = w; i < kWords; i += 4) {
-        const int64_t p = static_cast<int64_t>(chunk) * kChunk + 64 * i + lane;
-        const int u = p < a.num_pages ? a.uses[p] : 1;
-        const uint64_t word = __ballot(u <= 0);
-        if (p < a.num_pages && (u < 0 || a.uses_out != a.uses))
-            a.uses_out[p] = u > 0 ? u : 0;
+    const int64_t first = static_cast<int64_t>(chunk) * kChunk + 64 * w + lane;
+    int u[kWords / 4], n = 0;
+#pragma unroll
+    for (int k = 0; k < kWords / 4; ++k) {
+        const int64_t p = first + 256 * k;
+        u[k] = a.uses[p < a.num_pages ? p : a.num_pages - 1];
+    }
+#pragma unroll
+    for (int k = 0; k < kWords / 4; ++k) {
+        const int64_t p = first + 256 * k;
+        const uint64_t word = __ballot(p < a.num_pages && u[k] <= 0);
+        if (p < a.num_pages && (u[k] < 0 || a.uses_out != a.uses))
+            a.uses_out[p] = u[k] > 0 ? u[k] : 0;
         if (lane == 0)
-            a.bits[static_cast<int64_t>(chunk) * kWords + i] = word;
+            a.bits[static_cast<int64_t>(chunk) * kWords + w + 4 * k] = word;
         n += __popcll(word);  // the same in every lane
     }
     const int all = block_sum(lane == 0 ? n : 0, lds);
@@ -156,17 +177,18 @@ __device__ __forceinline__ int words_before(uint64_t word, int before)
 }
 
 // The free pages of ranks [from, from + n) into LDS (n up to kTake; -1 past the last), by a workgroup:
-// the chunks that hold them by a running sum of the counts, their words by one lane each.
+// the chunks that hold them by a running sum of the counts (`mine`: the thread's of the first 256),
+// their words by one lane each.
 constexpr int kTake = 1024;
 
-__device__ __forceinline__ void free_pages(const PoolArgs &a, int from, int n, int *out, int *lds)
+__device__ __forceinline__ void free_pages(const PoolArgs &a, int mine, int from, int n, int *out, int *lds)
 {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
     __syncthreads();  // `out` may still be read
     for (int i = threadIdx.x; i < n; i += 256)
         out[i] = -1;
     for (int c0 = 0, before = 0; c0 < a.chunks && before < from + n; c0 += 256) {
-        const int c = c0 + threadIdx.x, count = c < a.chunks ? a.counts[c] : 0;
+        const int c = c0 + threadIdx.x, count = c0 == 0 ? mine : c < a.chunks ? a.counts[c] : 0;
         int sum = count;
 #pragma unroll
         for (int y = 1; y < 64; y *= 2) {
@@ -201,11 +223,54 @@ __device__ __forceinline__ Span part_of(const PoolArgs &a, int part)
                 static_cast<int>(from + per < a.max_pages ? from + per : a.max_pages), 0};
 }
 
+// f(i, x[i], y[i]) for i in a part, by a workgroup; four of a thread are loaded before the first is used
+template <typename F>
+__device__ __forceinline__ void part_entries(const Span &part, const int *x, const int *y, F f)
+{
+    constexpr int U = 4;
+    for (int64_t i0 = part.from + threadIdx.x; i0 < part.to; i0 += 256 * U) {
+        int u[U], v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t i = i0 + 256 * k < part.to ? i0 + 256 * k : part.to - 1;
+            u[k] = x[i], v[k] = y[i];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i0 + 256 * k < part.to)
+                f(static_cast<int>(i0 + 256 * k), u[k], v[k]);
+    }
+}
+
+// The free pages of the pool, and what the streams in front of stream b need; for the first stream, what
+// all of them need. Loaded at a kernel's start, beside what the rest of it waits for, and summed later.
+struct Balance {
+    int count, need;  // of this thread: chunk threadIdx.x, and stream threadIdx.x of those that count
+    int free, needs;  // sums
+    __device__ __forceinline__ Balance(const PoolArgs &a, int b)
+        : count(static_cast<int>(threadIdx.x) < a.chunks ? a.counts[threadIdx.x] : 0),
+          need(static_cast<int>(threadIdx.x) < (b == 0 ? a.batch : b) ? a.needs[threadIdx.x] : 0), free(0), needs(0)
+    {
+    }
+    __device__ __forceinline__ void sum(const PoolArgs &a, int b, int *lds)  // lds: 8
+    {
+        int v[2] = {count, need};
+        for (int i = 256 + threadIdx.x; i < a.chunks; i += 256)
+            v[0] += a.counts[i];
+        for (int i = 256 + threadIdx.x, n = b == 0 ? a.batch : b; i < n; i += 256)
+            v[1] += a.needs[i];
+        block_sums(v, lds);
+        free = v[0], needs = v[1];
+    }
+};
+
 // Rows, a part of one each: gives back, takes, counts. The entries that new tokens start are the
-// first part's, so that none is ranked by a table that another workgroup has begun to fill.
+// first workgroup's of a row, so that none is ranked by a table that another one has begun to fill; a
+// row of several parts has one more workgroup for them, since both are chains of loads
+// (64 rows of 16,384 entries: 7.3 us, 6.5 so).
 __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
 {
-    __shared__ int lds[4], list[kTake];
+    __shared__ int lds[8], list[kTake];
     const int b = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     if (b >= a.p.batch) {  // no streams
         if (threadIdx.x == 0)
@@ -215,37 +280,36 @@ __global__ __launch_bounds__(256) void k_advance_rows(AdvanceArgs a)
     const int64_t row = static_cast<int64_t>(b) * a.p.max_pages;
     const int *in = a.p.table + row;
     int *out = a.p.table_out + row;
-    const Span s = new_entries(a, b), part = part_of(a.p, blockIdx.x);
-    for (int i = part.from + threadIdx.x; i < part.to; i += 256) {
+    Balance all(a.p, b);
+    const int own = a.p.needs[b];
+    const Span s = new_entries(a, b), none{};
+    const bool whole_row = gridDim.x == 1;
+    part_entries(whole_row ? part_of(a.p, 0) : blockIdx.x ? part_of(a.p, blockIdx.x - 1) : none, in, in, [&](int i, int e, int) {
         if (i >= s.from && i < s.to)
-            continue;
-        const int e = in[i];
+            return;
         const bool kept = stays(a, s, i, e);
         if (!kept && is_page(a.p, e))
             atomicSub(&a.p.uses_out[e], 1);
         if (in != out || !kept)
             out[i] = kept ? e : -1;
-    }
-    if (blockIdx.x != 0)
+    });
+    if (blockIdx.x != 0 || (b != 0 && s.from >= s.to))
         return;
-    const int free = sum_of(a.p.counts, a.p.chunks, lds);
-    if (b == 0) {
-        const int need = sum_of(a.p.needs, a.p.batch, lds);
-        if (threadIdx.x == 0)
-            a.lacking[0] = need > free ? need - free : 0;
-    }
-    if (s.from >= s.to)
-        return;
-    const int place = sum_of(a.p.needs, b, lds), own = a.p.needs[b];
+    auto entry = [&](int i) { return i < s.to ? in[i] : 0; };
+    int next = entry(s.from + threadIdx.x);
+    all.sum(a.p, b, lds);
+    if (b == 0 && threadIdx.x == 0)
+        a.lacking[0] = all.needs > all.free ? all.needs - all.free : 0;
+    const int place = b == 0 ? 0 : all.needs;
     int taken = 0, first = 0, listed = 0;  // of the stream's needs: met, and listed [first, listed)
     for (int i0 = s.from; i0 < s.to; i0 += 256) {
         if (taken + 256 > listed && listed < own) {  // the next 256 entries may need more than are listed
             listed = taken + kTake < own ? taken + kTake : own;
-            free_pages(a.p, place + taken, listed - taken, list, lds);
+            free_pages(a.p, all.count, place + taken, listed - taken, list, lds);
             first = taken;
         }
-        const int i = i0 + threadIdx.x;
-        const int e = i < s.to ? in[i] : 0;
+        const int i = i0 + threadIdx.x, e = next;
+        next = entry(i + 256);
         const bool empty = i < s.to && !is_page(a.p, e);
         const uint64_t word = __ballot(empty);
         __syncthreads();
@@ -299,13 +363,14 @@ __global__ __launch_bounds__(256) void k_fork_count(ForkArgs a)
 
 __global__ __launch_bounds__(256) void k_fork_rows(ForkArgs a)
 {
-    __shared__ int lds[4], list[1];
+    __shared__ int lds[8], list[1];
     if (a.p.batch == 0) {
         if (threadIdx.x == 0)
             a.lacking[0] = 0;
         return;
     }
     const int b = blockIdx.y, parent = a.parents[b], again = a.again[b], need = a.p.needs[b];
+    Balance all(a.p, b);
     const bool goes_on = parent >= 0 && parent < a.p.batch;
     const int len = goes_on ? cached(a.p, parent) : 0, whole = len >> a.p.page_shift;
     const Span part = part_of(a.p, blockIdx.x);
@@ -313,28 +378,25 @@ __global__ __launch_bounds__(256) void k_fork_rows(ForkArgs a)
     const int64_t row = static_cast<int64_t>(b) * a.p.max_pages;
     int fresh = -1;
     if (blockIdx.x == 0 || (need && whole >= part.from && whole < part.to)) {
-        const int free = sum_of(a.p.counts, a.p.chunks, lds);
+        all.sum(a.p, b, lds);
         if (need) {
-            free_pages(a.p, sum_of(a.p.needs, b, lds), 1, list, lds);
+            free_pages(a.p, all.count, b == 0 ? 0 : all.needs, 1, list, lds);
             fresh = list[0];
         }
-        if (blockIdx.x == 0) {
-            const int all = b == 0 ? sum_of(a.p.needs, a.p.batch, lds) : 0;
-            if (threadIdx.x == 0) {
-                if (b == 0)
-                    a.lacking[0] = all > free ? all - free : 0;
-                a.lens_out[b] = len;
-                a.copies[2 * static_cast<int64_t>(b)] = fresh >= 0 ? from[whole] : -1;
-                a.copies[2 * static_cast<int64_t>(b) + 1] = fresh;
-            }
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            if (b == 0)
+                a.lacking[0] = all.needs > all.free ? all.needs - all.free : 0;
+            a.lens_out[b] = len;
+            a.copies[2 * static_cast<int64_t>(b)] = fresh >= 0 ? from[whole] : -1;
+            a.copies[2 * static_cast<int64_t>(b) + 1] = fresh;
         }
     }
-    for (int i = part.from + threadIdx.x; i < part.to; i += 256) {
-        int e = goes_on && !(again && i >= whole) ? from[i] : -1;
+    part_entries(part, from, a.p.table + row, [&](int i, int e, int old) {
+        if (!goes_on || (again && i >= whole))
+            e = -1;
         if (need && i == whole)
             e = fresh;
         e = is_page(a.p, e) ? e : -1;
-        const int old = a.p.table[row + i];
         if (e != old) {
             if (e >= 0)
                 atomicAdd(&a.p.uses_out[e], 1);
@@ -342,7 +404,7 @@ __global__ __launch_bounds__(256) void k_fork_rows(ForkArgs a)
                 atomicSub(&a.p.uses_out[old], 1);
         }
         a.p.table_out[row + i] = e;
-    }
+    });
 }
 
 // ---- compact
@@ -433,10 +495,10 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a)
 // ---- one workgroup
 // The same calls where the pool, the table and the streams are small: one launch, since more cost more
 // than the work. Free pages and uses are held in LDS. Limits of pages and table entries together: an
-// advance of few takes 4.9 us here and 9.1 as two launches, of 16,000 9.0 and 10.7, of 32,000 14.3 and
-// 10.9; a compaction, three launches else, of 32,000 11.6 and 16.6, of 80,000 18.9 and 16.2.
+// advance of few takes 4.8 us here and 8.4 as two launches, of 16,000 9.0 and 9.4, of 32,000 14.2 and
+// 9.6; a compaction, three launches else, of 32,000 11.6 and 15.6, of 80,000 18.8 and 15.0.
 constexpr int kSmallPages = 16384, kSmallRows = 1024, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
-constexpr int64_t kSmallTake = 24576, kSmallCompact = 49152;
+constexpr int64_t kSmallTake = 16384, kSmallCompact = 49152;
 
 struct Small {
     int list[kSmallPages];  // free pages in order; compact: where a page goes, from page n on
@@ -866,7 +928,7 @@ extern "C" bdssm_status bdssm_pages_advance(const bdssm_pages_dims *dims, const 
     }
     if (a.p.chunks + dims->batch > 0)
         k_advance_count<<<a.p.chunks + dims->batch, 256, 0, st>>>(a);
-    k_advance_rows<<<dim3(a.p.row_parts, std::max(1, dims->batch)), 256, 0, st>>>(a);
+    k_advance_rows<<<dim3(a.p.row_parts + (a.p.row_parts > 1), std::max(1, dims->batch)), 256, 0, st>>>(a);
     return launched(hipGetLastError());
 }
 
