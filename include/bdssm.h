@@ -628,9 +628,10 @@ bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk
  *   first, last  [tokens] device int32 in the order of chunk rows, each or NULL (0, no end)
  * Errors as bdssm_attn_step; BDSSM_ERR_UNSUPPORTED also for a cap that is negative or not finite,
  * or for which scale / cap or cap itself is beyond 2^-126 to 2^126 or so, and for a scale outside
- * 2^-64 to 2^64 where slopes are given. out and workspace must not overlap these arrays. bdssm_attn_step_ex_workspace says what the call needs as
- * bdssm_attn_step_workspace does; of scores it looks at cap and at whether first and last are given,
- * not at what they hold: without ranges it is the same.
+ * 2^-64 to 2^64 where slopes are given. out and workspace must not overlap these arrays.
+ * bdssm_attn_step_ex_workspace says what the call needs as bdssm_attn_step_workspace does; of
+ * scores it looks at cap and at whether first and last are given, not at what they hold: without
+ * ranges it is the same.
  */
 typedef struct {
     float cap;
@@ -737,8 +738,9 @@ bdssm_status bdssm_rotary_append(const bdssm_attn_dims *dims, const bdssm_attn_c
  * No call reads a count that the host does not have: where pages run out, the entries that lack
  * one stay empty (-1) and lacking[0] says how many.
  * Errors: BDSSM_ERR_NULL, BDSSM_ERR_SHAPE, BDSSM_ERR_UNSUPPORTED (page_size, batch above 65535,
- * positions past 2^31, an advance that could need 2^31 pages), BDSSM_ERR_ALIGN (4 bytes;
- * workspace 16), BDSSM_ERR_ALIAS, BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The query returns SIZE_MAX for dims the calls reject.
+ * positions past 2^31, an advance that could need 2^31 pages), BDSSM_ERR_ALIGN (4 bytes; workspace
+ * 16), BDSSM_ERR_ALIAS, BDSSM_ERR_WORKSPACE, BDSSM_ERR_HIP. The query returns SIZE_MAX for dims the
+ * calls reject.
  */
 typedef struct {
     int32_t batch;     /* streams */

@@ -17,7 +17,7 @@ from test_gpu_attn import BF16, F32, Case, _case, _np, half_ulp
 pytestmark = pytest.mark.gpu
 
 
-def alibi(H):
+def slopes_of(H):
     return [2.0 ** (-8.0 * (h + 1) / H) for h in range(H)]
 
 
@@ -116,7 +116,7 @@ KINDS = {"cap": dict(cap=5.0), "bias": dict(slopes=True), "both": dict(cap=30.0,
 def scored(lens, counts, kind, H=4, **kw):
     more = dict(KINDS[kind])
     if more.get("slopes"):
-        more["slopes"] = alibi(H)
+        more["slopes"] = slopes_of(H)
     return Scored(lens, counts, H=H, **more, **kw)
 
 
@@ -186,7 +186,7 @@ def test_documents(dtype, block, kind):
     _case(f"documents block {block} dtype {dtype} {kind}")
     lens, counts = [0, 130, 7], [200, 100, 33]
     first, last = documents(lens, counts, [3, 4, 40, 64, 100, 150, 152, 200, 215])
-    more = {} if kind is None else dict(cap=30.0, slopes=alibi(4))
+    more = {} if kind is None else dict(cap=30.0, slopes=slopes_of(4))
     Scored(lens, counts, first=first, last=last, block=block, dtype=dtype, **more).check("documents")
     Scored(lens, counts, first=first, block=block, dtype=dtype, ragged=True, **more).check("first only")
     Scored(lens, counts, last=last, block=block, dtype=dtype, **more).check("last only")
@@ -237,7 +237,7 @@ def test_random_ranges(dtype, window, sinks, own_keys):
     first[5::13], last[5::13] = -2**31, 2**31 - 1
     first[6::17], last[6::17] = 2**31 - 1, -2**31
     c = Scored(lens, counts, first=list(map(int, first)), last=list(map(int, last)), window=window, sinks=sinks, block=1,
-               slopes=alibi(4), own_keys=own_keys, dtype=dtype)
+               slopes=slopes_of(4), own_keys=own_keys, dtype=dtype)
     c.check("ranges")
     out, empty = c.run(), [i for i in range(n) if last[i] <= first[i]]
     assert (out[empty] == 0).all()
@@ -273,7 +273,7 @@ def test_infinities_stay_with_their_document(dtype):
     _case(f"infinities dtype {dtype}")
     lens, counts = [100], [150]
     first, last = documents(lens, counts, [60, 120, 121, 200])
-    make = lambda: Scored(lens, counts, first=first, last=last, block=0, cap=10.0, slopes=alibi(4), dtype=dtype)  # noqa: E731
+    make = lambda: Scored(lens, counts, first=first, last=last, block=0, cap=10.0, slopes=slopes_of(4), dtype=dtype)  # noqa: E731
     plain = make().run()
     for at, bad in ((70, float("inf")), (130 - 100, float("nan")), (220 - 100, float("-inf"))):
         c = make()
