@@ -269,6 +269,18 @@ struct Poly {
 // Bias: a slope times the distance to the key. The softmax does not change when a row's scores
 // move together, so the distance is taken from the nearest position that the row attends to
 // (`from`): where a row sees only far keys, the common part, which float32 would round, is left out.
+// A slope beyond 2^26 counts as 2^26: the nearest key then has all of the weight, unless scores differ by
+// as much, and a slope times a distance (below 2^31), log2 e and the inverse of the scale (2^64 at most)
+// stays finite. An infinity at the first key of a block, from which the others step, would reach the
+// nearest. Where products start from the bias, one below -2^26 counts as that: weights are exp2 of one fma
+// of the raw score, and the rounding of a reference of 2^26.6 leaves 4 in its exponent (kAbove is more); of
+// one of 2^32, which a tile of far keys would set before the nearest comes, more than float32 holds.
+constexpr float kSteepest = 0x1p26f;
+__device__ __forceinline__ float slope_of(const AttnScoring &g, int head)
+{
+    const float s = g.slopes[head];
+    return fabsf(s) > kSteepest ? copysignf(kSteepest, s) : s;
+}
 __device__ __forceinline__ int bias_from(const Sight &x, int p, int sinks)
 {
     const int hi = x.lo < x.hi || x.hi < sinks ? x.hi : sinks;  // of the sinks where the window leaves nothing
@@ -335,7 +347,7 @@ __device__ __forceinline__ bool repair(const AttnArgs &a, const std::conditional
     for (int row = x.r_first + w; row < x.r_end; row += x.nwaves) {
         const int tok = a.by_group(row), head = x.kvh * G + row - tok * G;
         const Sight see = sight_of<EX>(a, s, end, prefix, tok);
-        const float slope = EX && a.score.slopes ? a.score.slopes[head] * kLog2e : 0.f;
+        const float slope = EX && a.score.slopes ? slope_of(a.score, head) * kLog2e : 0.f;
         const T *q = static_cast<const T *>(a.q) + (s.row0 + tok) * a.q_stride + static_cast<int64_t>(head) * D;
         float m = -__builtin_inff(), l = 0.f, o[PL] = {};
         for (int t = x.t0; t < x.t1; ++t) {
@@ -677,7 +689,7 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     float m = -__builtin_inff(), l = 0.f;
     const float sc = RAW ? a.scale * kLog2e : 1.f;  // of scores as `raise` and `weigh` find them
     const bool bias = EX && a.score.slopes;
-    float slope = bias ? a.score.slopes[head] * (RAW ? 1.f / a.scale : kLog2e) : 0.f;
+    float slope = bias ? slope_of(a.score, head) * (RAW ? 1.f / a.scale : kLog2e) : 0.f;
     const int from = bias_from(my, s.len + tok, a.sinks) - 4 * hf;
 
     // ---- operand reads. Every lane offset is one opaque value, a single step from its array:
@@ -706,9 +718,17 @@ __attribute__((amdgpu_waves_per_eu(WPE, WPE))) void k_attn(AttnArgs a, AttnPlan 
     f32x16 sv[KB];               // scores
     // the bias of block kb's key r of a lane: -slope |from - j|. Keys of the cache that a row sees are
     // not past `from` (either `from` is the row's own position or later, or it is its last key)
+    const bool steep = MODE == kRanged && RAW && bias && __ballot(fabsf(slope) * a.scale * static_cast<float>(end) > kSteepest) != 0;
     auto biased = [&](auto S, int kb, auto with) {
         const int d = from - jpos[S.value] - 32 * (wk * KB + kb);
-        if (jpos[S.value] < s.len) {
+        if (steep) {
+            float scale = a.scale;
+            asm volatile("" : "+v"(scale));  // made here, not kept through the loop
+            const float least = -kSteepest / scale;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sv[kb][r] = with(fmaxf(-slope * fabsf(static_cast<float>(d - 8 * (r / 4) - r % 4)), least), r);
+        } else if (jpos[S.value] < s.len) {
             // key r is 8 (r / 4) + r % 4 further on. In steps of 1, 2 and 4 slopes, which instructions
             // hold themselves; other factors would take a register each
             float b = -slope * static_cast<float>(d);

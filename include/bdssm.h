@@ -623,7 +623,9 @@ bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk
  * Workgroups skip keys that the ranges of all their rows leave out, so that documents packed
  * into one chunk cost what they cost apart.
  *   cap       0 (none) or > 0, finite
- *   slopes    [nheads] device float32, finite, or NULL
+ *   slopes    [nheads] device float32, finite, or NULL. Scores with their bias are held up to 2^26 in
+ *             magnitude: a slope beyond that counts as 2^26 and a bias below -2^26 as that (or as
+ *             itself), so that a steep slope leaves the nearest key all of a row's weight
  *   prefix    [batch] device int32, or NULL
  *   first, last  [tokens] device int32 in the order of chunk rows, each or NULL (0, no end)
  * Errors as bdssm_attn_step; BDSSM_ERR_UNSUPPORTED also for a cap that is negative or not finite,
