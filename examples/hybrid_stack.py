@@ -176,17 +176,18 @@ class HybridStack:
             bdssm.pages_copy(self.attn, layer.cache, copies)
 
     def fork(self, parents):
-        """Stream b becomes a continuation of stream parents[b] (an int32 tensor); pages have to be
-        managed."""
+        """Stream b becomes a continuation of stream parents[b] (an int32 tensor), or empty where that is
+        no stream; pages have to be managed."""
         table, copies = torch.empty_like(self.table), torch.empty((self.batch, 2), dtype=torch.int32, device="cuda")
         bdssm.pages_fork(self.page_dims, self.books(), parents, table, self.lens[1], self.uses, copies, self.lacking,
                          self.pages_ws)
         self._take(table, copies)
         self.lens[0].copy_(self.lens[1])
-        rows = parents.long()
+        rows = parents.long().clamp(0, self.batch - 1)
+        ended = ((parents < 0) | (parents >= self.batch)).view(-1, 1, 1, 1)
         for layer in self.layers:
             if isinstance(layer, MambaLayer):
-                layer.state.copy_(layer.state[rows])
+                layer.state.copy_(layer.state[rows].masked_fill(ended, 0.0))
                 bdssm.state_ops(layer.dims, layer.state, layer.ops)
 
     def compact(self):
