@@ -132,6 +132,8 @@ AttnPlan attn_plan(const AttnArgs &a, int D, bool bf16);
 // the length: a longer cache may fit whole rounds of workgroups with fewer ranges. SIZE_MAX: more
 // rows than a launch has threads for.
 size_t attn_workspace(const AttnArgs &a, int D, bool bf16);
+// The order of nrt row tiles (of `rows` rows, their keys in tiles of tk) of every stream (attn_ranged.hip).
+void launch_attn_order(const AttnArgs &a, int nrt, int rows, int tk, int shift, int *order, hipStream_t st);
 hipError_t launch_attn(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 hipError_t launch_attn_ranged(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
 hipError_t launch_attn_capped(const AttnArgs &a, int D, bool bf16, const AttnPlan &p, void *ws, hipStream_t st);
