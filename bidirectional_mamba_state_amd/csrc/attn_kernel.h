@@ -48,9 +48,15 @@
 //    740 on unequal ones (64 x 16-32K tokens, 768 rows: 1.23 ms), where short row tiles leave
 //    wavefronts idle;
 //  - float32: the matrix cores, 100 to 125 TFLOP/s;
-//  - a cap: the vector unit beside them (48 % busy, matrix cores 34 %): the prompt chunk 1.27 ms, the
-//    unequal streams 1.78; a bias: the prompt chunk 1.23 ms, the unequal streams 1.36, where the vector
-//    unit is 69 % busy; both: 1.69 and 2.07 ms.
+//  - a cap: the vector unit beside them (48 % busy, matrix cores 34 %): the prompt chunk 1.30 ms, the
+//    unequal streams 1.84; a bias: the prompt chunk 1.23 ms, the unequal streams 1.37, where the vector
+//    unit is 68 % busy; both: 1.70 and 2.12 ms. At headdim 64 these kernels spill 7 (bias) and 8 (cap)
+//    of their 128 registers, the plain one none;
+//  - documents packed into a prompt (8,191 tokens in some of 700, 16 heads over 4): neither unit (vector
+//    46 and 36 % busy, matrix cores 18 and 24 % at headdim 64 and 128; waits 38 and 35 %): a workgroup
+//    walks seven tiles on average, behind its start; 41 and 60 us, 5.7 of them the order of row tiles.
+//    As streams of their own they take 34 and 52 us (documents of 60 to 2,000: packed 0.7 to 1.3 times
+//    that).
 // Eight wavefronts of 32 rows, four a SIMD at headdim 64, did better than four of 64 (half the
 // LDS reads, but nothing hides a wavefront's own exponentials: 1340 against 1020 us on the
 // prompt), than a third stage, 128-key tiles or a scheduled overlap inside a wavefront (no
@@ -212,13 +218,14 @@ enum Mode { kPlain, kRanged, kCapped, kExact };
 // some |x|; and 1 - 2 / (1 + e^2x), whose error is a few 2^-24 of c, and which an infinite score takes
 // to +-1. Each costs: the polynomial a multiplication and an addition a term, the other two
 // transcendentals, which take as long as eight additions.
-//  - kExact: six terms up to 0.6 (2.5e-9), the other form from there on, where it is a few 2^-24 of the
+//  - kExact: six terms up to 0.6 (5e-9), the other form from there on, where it is a few 2^-24 of the
 //    score too; of both, where a wavefront's scores of a tile are not all small, the one that applies.
 //  - kCapped: the other form (a few 2^-24 of c). At headdim 128, where a wavefront sees a whole tile and
 //    all of its scores are below c / 2, four terms instead (5.4e-7 of the score: up to 1e-4 of a power
 //    of two, a fortieth of the rounding of a bf16 weight), made along with the weights, where the
 //    products hide them (a prompt of 8,192 on 8,192: 1.30 ms, 1.48 in the other form, 2.0 in front of
-//    the weights). At 64 a wavefront has no registers for both ways: what is saved goes into spills.
+//    the weights). At 64 the 8 x 1 shape's registers are full (8 spilled, 36 bytes a lane): with both ways
+//    more spills took what was saved.
 //
 // Constants are operands of the instructions themselves (add_mul): as values each took a vector
 // register through the loop over tiles.
@@ -1211,7 +1218,8 @@ void join(const AttnArgs &a, int nsplit, const float *part, const float2 *ml, hi
 //         as 1 x 4 with tiles of 128 is no faster: 6 rows on 255 keys 8.4 us, 8.9 so, on 1,000 keys
 //         of headdim 128 12.1, 15.6 so, on 16,384 keys the same. More, where rows have ranges of
 //         their own: 4 x 1, which waste less at a document's borders (8,191 tokens of 16 heads over 4
-//         in documents of 700, headdim 128: 72 us, 81 as 8 x 1; in one: 205 and 230)
+//         in documents of 700: 41 us, 47 as 8 x 1; headdim 128 60 and 67; in one document 194 and
+//         207, at headdim 128 307 and 297)
 //  f32    up to 32 rows of headdim 64: 1 x 4 (32 rows, 8 streams of 4,096: 28 us, 32 us as 2 x 2,
 //         47 us as 4 x 1); up to 64 rows: 2 x 2 (64 rows: 34 us, 49 us as 4 x 1; headdim 128:
 //         58 us, 83 us); more: 4 x 1, whose products leave no room for more wavefronts

@@ -70,7 +70,7 @@ __device__ __forceinline__ void turn_pair(T &a, T &b, float2 t)
 // A workgroup takes `tok` tokens of one stream. The scaled cosines and sines of their pairs are
 // made once, in LDS, for all heads; the threads walk the units of (token, head): queries, keys,
 // values. Bound by the rows' bytes: a step of 34,000 tokens of 20 + 4 heads x 128 takes 62 us, 6.8
-// TB/s both ways (a large copy by the library: 4.9), with values and into pages 78 us, 6.3. What that
+// TB/s both ways (a large copy by the library: 4.9), with values and into pages 75 us, 6.5. What that
 // took: four pieces of a thread in flight (two: 122 us), 4 tokens a workgroup (16, whose first loads
 // nothing covers: 112 us; eight pieces in flight no better), and, where the outputs are more than the
 // L2s hold, stores that do not stay in them (STREAM; 101 us without). One block of 32: 2.9 us, the

@@ -621,7 +621,7 @@ bdssm_status bdssm_kv_append(const bdssm_attn_dims *dims, const bdssm_attn_chunk
  * Positions outside the stream's keys are taken as their nearest end. Distances are exact up to
  * 2^24 and count from the nearest position that the query's window, order and range leave.
  * Workgroups skip keys that the ranges of all their rows leave out, so that documents packed
- * into one chunk cost what they cost apart.
+ * into one chunk cost about what they cost as streams of their own.
  *   cap       0 (none) or > 0, finite
  *   slopes    [nheads] device float32, finite, or NULL. Scores with their bias are held up to 2^26 in
  *             magnitude: a slope beyond that counts as 2^26 and a bias below -2^26 as that (or as
